@@ -16,6 +16,8 @@ Names follow the C ABI:
   int8_mixed_matmul  a6  LLM.int8() mixed decomposition
   fold_norm          1/s folded into the preceding norm's gamma / beta
   norm_quantize_act  fused fp16 norm -> int8 (per-token or per-tensor)
+Microscaled forms (``include/sq_mx.h``): quantize_act_mx,
+smooth_weights_mxfp4, norm_quantize_act_mx, dequantize_mx, gemm_mxfp4.
 """
 from __future__ import annotations
 
@@ -26,11 +28,13 @@ import re
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libsq.so")
 HEADER = os.path.join(os.path.dirname(HERE), "include", "sq.h")
+MX_HEADER = os.path.join(os.path.dirname(HERE), "include", "sq_mx.h")
 TEST_HEADER = os.path.join(os.path.dirname(HERE), "include", "sq_test.h")
 
 SQ_F32, SQ_F16, SQ_BF16 = 0, 1, 2
 SQ_PER_TENSOR_STATIC, SQ_PER_TOKEN_DYNAMIC = 0, 1
 SQ_NORM_LAYER, SQ_NORM_RMS = 0, 1
+SQ_MX_E2M1, SQ_MX_E4M3 = 0, 1
 
 _lib = None
 
@@ -61,6 +65,12 @@ SIGNATURES = {
     "sq_smooth_weights_fp8": (_I, [_P, _I, _I64, _I64, _P, _P, _P, _P]),
     "sq_quantize_act_fp8": (_I, [_P, _I, _I64, _I64, _P, _I, _P, _P, _P, _P]),
     "sq_gemm_fp8_dequant": (_I, [_P, _P, _I64, _I64, _I64, _P, _I, _P, _P, _I, _P]),
+    # microscaled forms (include/sq_mx.h)
+    "sq_quantize_act_mx": (_I, [_P, _I, _I64, _I64, _P, _I, _P, _P, _P]),
+    "sq_smooth_weights_mxfp4": (_I, [_P, _I, _I64, _I64, _P, _P, _P, _P, _P]),
+    "sq_norm_quantize_act_mx": (_I, [_P, _I, _I64, _I64, _I, _P, _P, _F, _I, _P, _P, _P]),
+    "sq_dequantize_mx": (_I, [_P, _P, _I, _I64, _I64, _P, _I, _P]),
+    "sq_gemm_mxfp4": (_I, [_P, _P, _I, _P, _P, _I64, _I64, _I64, _P, _I, _P]),
     # coverage entry points (include/sq_test.h): the tiled GEMM's block shape forced
     "sq_gemm_i8_dequant_tile": (_I, [_P, _P, _I64, _I64, _I64, _P, _I, _P, _P, _I, _P, _P, _I]),
     "sq_gemm_fp8_dequant_tile": (_I, [_P, _P, _I64, _I64, _I64, _P, _I, _P, _P, _I, _P, _I]),
@@ -438,4 +448,143 @@ def gemm_fp8_dequant(xq, wq, x_scale, w_scale, out_dtype=None, out=None, stream=
         _call("sq_gemm_fp8_dequant_tile", xq.data_ptr(), wq.data_ptr(), M, N, K,
               x_scale.data_ptr(), int(per_row), w_scale.data_ptr(), y.data_ptr(), _dt(y),
               _stream(stream), int(tile))
+    return y
+
+
+# ------------------------------------------------------- microscaled (MX)
+
+def _mx_call(name, tensors, args, stream):
+    """Call `name` on the operands' own GPU.  `tensors` are all the operands
+    (None allowed); `stream` (or that GPU's current stream) gets the work."""
+    torch = _torch()
+    dev = next(t for t in tensors if t is not None).device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"operands on {dev} and {t.device}")
+    if torch.cuda.current_device() == dev.index:
+        _call(name, *args, _stream(stream))
+    else:
+        with torch.cuda.device(dev):
+            _call(name, *args, _stream(stream))
+
+
+def _mx_codes(fmt, K):
+    """Code bytes of a row of K elements."""
+    if fmt not in (SQ_MX_E2M1, SQ_MX_E4M3):
+        raise ValueError(f"unknown MX format {fmt}")
+    return K // 2 if fmt == SQ_MX_E2M1 else K
+
+
+def _mx_shapes(q, scale, fmt, name):
+    """(rows, K) of codes [rows, K / 2] or [rows, K] and scales [rows, K / 32]."""
+    torch = _torch()
+    _check(q, name, (torch.uint8,), 2)
+    _check(scale, f"{name}'s scales", (torch.uint8,), 2)
+    rows, K = q.shape[0], scale.shape[1] * 32
+    if tuple(q.shape) != (rows, _mx_codes(fmt, K)) or scale.shape[0] != rows:
+        raise ValueError(f"{name} {tuple(q.shape)} and its scales {tuple(scale.shape)} disagree")
+    return rows, K
+
+
+def _mx_out(out, rows, K, fmt, device):
+    torch = _torch()
+    if K % 32:
+        raise ValueError(f"rows of {K} elements: a multiple of 32 is needed")
+    if out is None:
+        return (torch.empty((rows, _mx_codes(fmt, K)), dtype=torch.uint8, device=device),
+                torch.empty((rows, K // 32), dtype=torch.uint8, device=device))
+    q, scale = out
+    if _mx_shapes(q, scale, fmt, "out") != (rows, K):
+        raise ValueError(f"out {tuple(q.shape)} does not fit {rows} rows of {K} elements")
+    return q, scale
+
+
+def _vector(t, name, n):
+    """The pointer of an fp32 vector of n elements, or None."""
+    if t is None:
+        return None
+    _check(t, name, (_torch().float32,), 1)
+    if t.numel() != n:
+        raise ValueError(f"{name} has {t.numel()} elements, not {n}")
+    return t.data_ptr()
+
+
+def _mx_rows(x, name):
+    torch = _torch()
+    x2 = x.reshape(-1, x.shape[-1])
+    _check(x2, name, (torch.float32, torch.float16, torch.bfloat16))
+    return x2
+
+
+def quantize_act_mx(x, inv_s=None, fmt=SQ_MX_E2M1, out=None, stream=None):
+    """a4 in MX: (xq uint8 [M, K/2] or [M, K], x_scale uint8 [M, K/32]) of
+    fl(x * inv_s), a power-of-two scale for each 32 elements."""
+    x2 = _mx_rows(x, "x")
+    M, K = x2.shape
+    inv = _vector(inv_s, "inv_s", K)
+    xq, xs = _mx_out(out, M, K, fmt, x2.device)
+    _mx_call("sq_quantize_act_mx", (x2, inv_s, xq, xs),
+             (x2.data_ptr(), _dt(x2), M, K, inv, int(fmt), xq.data_ptr(), xs.data_ptr()), stream)
+    return xq, xs
+
+
+def smooth_weights_mxfp4(w, s=None, row_mul=None, out=None, stream=None):
+    """a3 in MX: (wq uint8 [N, K/2] e2m1, w_scale uint8 [N, K/32]) of
+    fl(fl(w * row_mul[n]) * s[k]); row_mul and s as in smooth_weights."""
+    torch = _torch()
+    _check(w, "w", (torch.float32, torch.float16, torch.bfloat16), 2)
+    N, K = w.shape
+    sp, rp = _vector(s, "s", K), _vector(row_mul, "row_mul", N)
+    wq, ws = _mx_out(out, N, K, SQ_MX_E2M1, w.device)
+    _mx_call("sq_smooth_weights_mxfp4", (w, s, row_mul, wq, ws),
+             (w.data_ptr(), _dt(w), N, K, rp, sp, wq.data_ptr(), ws.data_ptr()), stream)
+    return wq, ws
+
+
+def norm_quantize_act_mx(x, gamma, beta=None, norm=SQ_NORM_LAYER, eps=1e-5, fmt=SQ_MX_E2M1,
+                         out=None, stream=None):
+    """Fused norm -> MX codes: (xq, x_scale) as quantize_act_mx."""
+    x2 = _mx_rows(x, "x")
+    M, K = x2.shape
+    if gamma is None:
+        raise ValueError("gamma is needed")
+    g, b = _vector(gamma, "gamma", K), _vector(beta, "beta", K)
+    xq, xs = _mx_out(out, M, K, fmt, x2.device)
+    _mx_call("sq_norm_quantize_act_mx", (x2, gamma, beta, xq, xs),
+             (x2.data_ptr(), _dt(x2), M, K, int(norm), g, b, float(eps), int(fmt), xq.data_ptr(),
+              xs.data_ptr()), stream)
+    return xq, xs
+
+
+def dequantize_mx(q, scale, fmt=SQ_MX_E2M1, out_dtype=None, out=None, stream=None):
+    """The values [rows, K] (fp32 unless out_dtype says otherwise) that MX
+    codes and scales stand for."""
+    torch = _torch()
+    rows, K = _mx_shapes(q, scale, fmt, "q")
+    y = out if out is not None else torch.empty((rows, K), dtype=out_dtype or torch.float32,
+                                                device=q.device)
+    _check(y, "out", (torch.float32, torch.float16, torch.bfloat16), 2)
+    if tuple(y.shape) != (rows, K):
+        raise ValueError(f"out {tuple(y.shape)} is not {(rows, K)}")
+    _mx_call("sq_dequantize_mx", (q, scale, y),
+             (q.data_ptr(), scale.data_ptr(), int(fmt), rows, K, y.data_ptr(), _dt(y)), stream)
+    return y
+
+
+def gemm_mxfp4(xq, x_scale, wq, w_scale, x_fmt=SQ_MX_E2M1, out_dtype=None, out=None, stream=None):
+    """a5 in MX: y [M, N] (fp16 unless out_dtype says otherwise), the product
+    of e2m1 weights with activations of x_fmt, summed in fp32."""
+    torch = _torch()
+    M, K = _mx_shapes(xq, x_scale, x_fmt, "xq")
+    N, Kw = _mx_shapes(wq, w_scale, SQ_MX_E2M1, "wq")
+    if K != Kw:
+        raise ValueError(f"K mismatch: xq has {K}, wq {Kw}")
+    y = out if out is not None else torch.empty((M, N), dtype=out_dtype or torch.float16,
+                                                device=xq.device)
+    _check(y, "out", (torch.float32, torch.float16, torch.bfloat16), 2)
+    if tuple(y.shape) != (M, N):
+        raise ValueError(f"out {tuple(y.shape)} is not {(M, N)}")
+    _mx_call("sq_gemm_mxfp4", (xq, x_scale, wq, w_scale, y),
+             (xq.data_ptr(), x_scale.data_ptr(), int(x_fmt), wq.data_ptr(), w_scale.data_ptr(), M,
+              N, K, y.data_ptr(), _dt(y)), stream)
     return y

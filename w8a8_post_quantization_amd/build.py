@@ -20,7 +20,8 @@ LIB_PATH = os.path.join(HERE, "libsq.so")
 PEAKS_LIB_PATH = os.path.join(HERE, "libsq_peaks.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
-SOURCES = ["reduce.hip", "quant.hip", "gemm.hip", "norm.hip", "sq_api.cpp"]
+SOURCES = ["reduce.hip", "quant.hip", "gemm.hip", "norm.hip", "sq_api.cpp",
+           "mx_quant.hip", "mx_norm.hip", "mx_gemm.hip", "sq_mx_api.cpp"]
 PEAK_SOURCES = ["peaks.hip"]
 FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-ffp-contract=off",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",

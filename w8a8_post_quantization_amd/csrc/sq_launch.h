@@ -89,6 +89,19 @@ void launch_norm_quant(const void *x, int64_t M, int64_t K, int norm, const floa
                        const float *beta, float eps, int dynamic, const float *static_scale,
                        int8_t *q, float *scale, hipStream_t stream, int force_kernel = -1);
 
+// Microscaled (MX) forms (include/sq_mx.h); fmt 0 e2m1, 1 e4m3.
+void launch_quant_mx(const void *x, int dt, int64_t rows, int64_t K, const float *mul,
+                     const float *row_mul, int fmt, uint8_t *q, uint8_t *scale,
+                     hipStream_t stream);  // row_mul: e2m1 only
+void launch_dequant_mx(const uint8_t *q, const uint8_t *scale, int fmt, int64_t rows, int64_t K,
+                       void *y, int y_dt, hipStream_t stream);
+void launch_norm_quant_mx(const void *x, int dt, int64_t M, int64_t K, int norm,
+                          const float *gamma, const float *beta, float eps, int fmt, uint8_t *q,
+                          uint8_t *scale, hipStream_t stream);
+void launch_gemm_mx(const uint8_t *xq, const uint8_t *xs, int x_fmt, const uint8_t *wq,
+                    const uint8_t *ws, int64_t M, int64_t N, int64_t K, void *y, int y_dt,
+                    hipStream_t stream);
+
 // Tiny device-to-device copies done by a kernel (no copy-engine or memset
 // nodes, so the calls stay capturable in a HIP graph).
 void launch_copy_f32(const float *src, float *dst, hipStream_t stream);
