@@ -89,6 +89,8 @@ def test_exports_every_declared_symbol():
                         "sq_quantize_act_mx", "sq_smooth_weights_mxfp4"]
     for name in declared:
         assert hasattr(L, name) and name in sq.SIGNATURES, name
+    assert sq.header_functions(sq.MX_TEST_HEADER) == ["sq_gemm_mxfp4_tile"]
+    assert hasattr(L, "sq_gemm_mxfp4_tile")
 
 
 @built
@@ -177,6 +179,10 @@ def test_gemm_validation():
     assert call(xs=FAKE + 2) == ALIGN and call(ws=FAKE + 1) == ALIGN
     assert call(y=FAKE + 2) == ALIGN
     assert call(M=0, x=None, y=None) == OK and call(N=0, w=None, y=None) == OK
+    assert call(K=(1 << 20) + 32) == UNSUP
+    for bad in (-2, 3):
+        assert sq.lib().sq_gemm_mxfp4_tile(FAKE, FAKE, 0, FAKE, FAKE, 64, 64, 256, FAKE, sq.SQ_F32,
+                                           None, bad) == ARG
 
 
 def test_binding_refuses_host_tensors():

@@ -309,6 +309,51 @@ def test_product_parity(torch, M, N, K, ydt, spread, fmt):
 
 
 @pytest.mark.parametrize("fmt", ["e2m1", "e4m3"])
+@pytest.mark.parametrize("tile", [0, 1, 2])
+@pytest.mark.parametrize("M,N,K,ydt", [
+    (40, 100, 256, "f32"), (300, 333, 384, "bf16"), (513, 520, 512, "f32"), (33, 260, 640, "f16"),
+    (129, 1030, 1152, "f32"), (256, 256, 1280, "bf16"), (700, 130, 4224, "f32")])
+def test_product_tiles(torch, M, N, K, ydt, tile, fmt):
+    """Every block shape of the pipelined kernel: fewer stages than its ring,
+    as many and more, with and without a last half stage, ragged edges."""
+    f = FMT[fmt]
+    xq, xs = _codes(M * 7 + K, M, K, f, 1)
+    if f == ref.E4M3:
+        xs = (xs - 7).astype(np.uint8)
+    wq, ws = _codes(N * 9 + K, N, K, ref.E2M1, 1)
+    if ydt == "f16":
+        ws = (ws - 6).astype(np.uint8)
+    xs[3, K // 32 - 1] = 255
+    ws[N - 1, K // 32 - 5] = 255
+    tdt = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}[ydt]
+    log(f"gemm_mxfp4 tile={tile} M={M} N={N} K={K} y={ydt} {fmt}")
+    y = sq.gemm_mxfp4(*[dev(a, torch) for a in (xq, xs, wq, ws)], f, out_dtype=tdt, tile=tile)
+    _check_product(host(y, torch), ydt, xq, xs, f, wq, ws)
+
+
+# Decode (M <= 32): every window width, windows past K, several windows a
+# wave, one to eight groups of rows a block and more than one round of blocks.
+@pytest.mark.parametrize("fmt", ["e2m1", "e4m3"])
+@pytest.mark.parametrize("M,N,K", [
+    (1, 5000, 992), (4, 20000, 544), (16, 33000, 1024), (31, 9000, 1056), (2, 13000, 1984),
+    (9, 300, 4064), (20, 26000, 2080), (7, 70000, 352), (3, 7001, 6016), (32, 12345, 8224),
+    (1, 100, 20000), (17, 40, 40000), (12, 4500, 16416)])
+def test_product_decode(torch, M, N, K, fmt):
+    f = FMT[fmt]
+    xq, xs = _codes(M * 13 + K, M, K, f, 1)
+    if f == ref.E4M3:
+        xs = (xs - 7).astype(np.uint8)
+    wq, ws = _codes(N * 17 + K, N, K, ref.E2M1, 1)
+    xs[M - 1, K // 64] = 255 if M > 3 else xs[M - 1, K // 64]
+    ws[N - 1, K // 32 - 1] = 255
+    log(f"gemm_mxfp4 decode M={M} N={N} K={K} {fmt}")
+    d = [dev(a, torch) for a in (xq, xs, wq, ws)]
+    y = host(sq.gemm_mxfp4(*d, f, out_dtype=torch.float32), torch)
+    n = np.unique(np.r_[0:min(N, 700), max(0, N - 700):N, N // 2:min(N, N // 2 + 300)])
+    _check_product(y[:, n], "f32", xq, xs, f, wq[n], ws[n])
+
+
+@pytest.mark.parametrize("fmt", ["e2m1", "e4m3"])
 @pytest.mark.parametrize("M,N,K", [(3, 50, 160), (40, 70, 96), (130, 140, 256)])
 def test_product_writes_its_rows_only(torch, M, N, K, fmt):
     """Guard rows before and after y, and an odd first element (y needs only

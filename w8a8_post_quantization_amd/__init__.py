@@ -29,6 +29,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libsq.so")
 HEADER = os.path.join(os.path.dirname(HERE), "include", "sq.h")
 MX_HEADER = os.path.join(os.path.dirname(HERE), "include", "sq_mx.h")
+MX_TEST_HEADER = os.path.join(os.path.dirname(HERE), "include", "sq_mx_test.h")
 TEST_HEADER = os.path.join(os.path.dirname(HERE), "include", "sq_test.h")
 
 SQ_F32, SQ_F16, SQ_BF16 = 0, 1, 2
@@ -71,6 +72,8 @@ SIGNATURES = {
     "sq_norm_quantize_act_mx": (_I, [_P, _I, _I64, _I64, _I, _P, _P, _F, _I, _P, _P, _P]),
     "sq_dequantize_mx": (_I, [_P, _P, _I, _I64, _I64, _P, _I, _P]),
     "sq_gemm_mxfp4": (_I, [_P, _P, _I, _P, _P, _I64, _I64, _I64, _P, _I, _P]),
+    # coverage entry point (include/sq_mx_test.h): the pipelined product's block shape forced
+    "sq_gemm_mxfp4_tile": (_I, [_P, _P, _I, _P, _P, _I64, _I64, _I64, _P, _I, _P, _I]),
     # coverage entry points (include/sq_test.h): the tiled GEMM's block shape forced
     "sq_gemm_i8_dequant_tile": (_I, [_P, _P, _I64, _I64, _I64, _P, _I, _P, _P, _I, _P, _P, _I]),
     "sq_gemm_fp8_dequant_tile": (_I, [_P, _P, _I64, _I64, _I64, _P, _I, _P, _P, _I, _P, _I]),
@@ -453,19 +456,20 @@ def gemm_fp8_dequant(xq, wq, x_scale, w_scale, out_dtype=None, out=None, stream=
 
 # ------------------------------------------------------- microscaled (MX)
 
-def _mx_call(name, tensors, args, stream):
+def _mx_call(name, tensors, args, stream, *last):
     """Call `name` on the operands' own GPU.  `tensors` are all the operands
-    (None allowed); `stream` (or that GPU's current stream) gets the work."""
+    (None allowed); `stream` (or that GPU's current stream) gets the work;
+    `last` are the arguments behind the stream."""
     torch = _torch()
     dev = next(t for t in tensors if t is not None).device
     for t in tensors:
         if t is not None and t.device != dev:
             raise ValueError(f"operands on {dev} and {t.device}")
     if torch.cuda.current_device() == dev.index:
-        _call(name, *args, _stream(stream))
+        _call(name, *args, _stream(stream), *last)
     else:
         with torch.cuda.device(dev):
-            _call(name, *args, _stream(stream))
+            _call(name, *args, _stream(stream), *last)
 
 
 def _mx_codes(fmt, K):
@@ -571,9 +575,11 @@ def dequantize_mx(q, scale, fmt=SQ_MX_E2M1, out_dtype=None, out=None, stream=Non
     return y
 
 
-def gemm_mxfp4(xq, x_scale, wq, w_scale, x_fmt=SQ_MX_E2M1, out_dtype=None, out=None, stream=None):
+def gemm_mxfp4(xq, x_scale, wq, w_scale, x_fmt=SQ_MX_E2M1, out_dtype=None, out=None, stream=None,
+               tile=None):
     """a5 in MX: y [M, N] (fp16 unless out_dtype says otherwise), the product
-    of e2m1 weights with activations of x_fmt, summed in fp32."""
+    of e2m1 weights with activations of x_fmt, summed in fp32.  tile (tests
+    only) forces the block shape (include/sq_mx_test.h)."""
     torch = _torch()
     M, K = _mx_shapes(xq, x_scale, x_fmt, "xq")
     N, Kw = _mx_shapes(wq, w_scale, SQ_MX_E2M1, "wq")
@@ -584,7 +590,10 @@ def gemm_mxfp4(xq, x_scale, wq, w_scale, x_fmt=SQ_MX_E2M1, out_dtype=None, out=N
     _check(y, "out", (torch.float32, torch.float16, torch.bfloat16), 2)
     if tuple(y.shape) != (M, N):
         raise ValueError(f"out {tuple(y.shape)} is not {(M, N)}")
-    _mx_call("sq_gemm_mxfp4", (xq, x_scale, wq, w_scale, y),
-             (xq.data_ptr(), x_scale.data_ptr(), int(x_fmt), wq.data_ptr(), w_scale.data_ptr(), M,
-              N, K, y.data_ptr(), _dt(y)), stream)
+    args = (xq.data_ptr(), x_scale.data_ptr(), int(x_fmt), wq.data_ptr(), w_scale.data_ptr(), M, N,
+            K, y.data_ptr(), _dt(y))
+    if tile is None:
+        _mx_call("sq_gemm_mxfp4", (xq, x_scale, wq, w_scale, y), args, stream)
+    else:
+        _mx_call("sq_gemm_mxfp4_tile", (xq, x_scale, wq, w_scale, y), args, stream, int(tile))
     return y

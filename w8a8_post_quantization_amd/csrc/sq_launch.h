@@ -100,7 +100,7 @@ void launch_norm_quant_mx(const void *x, int dt, int64_t M, int64_t K, int norm,
                           uint8_t *scale, hipStream_t stream);
 void launch_gemm_mx(const uint8_t *xq, const uint8_t *xs, int x_fmt, const uint8_t *wq,
                     const uint8_t *ws, int64_t M, int64_t N, int64_t K, void *y, int y_dt,
-                    hipStream_t stream);
+                    hipStream_t stream, int force_tile = -1);
 
 // Tiny device-to-device copies done by a kernel (no copy-engine or memset
 // nodes, so the calls stay capturable in a HIP graph).

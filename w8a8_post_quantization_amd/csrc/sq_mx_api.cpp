@@ -1,6 +1,7 @@
 // C ABI of the microscaled operators (include/sq_mx.h): argument validation
 // on the host, then kernel launches on the caller's stream.
 #include "../../include/sq_mx.h"
+#include "../../include/sq_mx_test.h"
 
 #include <hip/hip_runtime.h>
 
@@ -87,20 +88,28 @@ int sq_dequantize_mx(const uint8_t *q, const uint8_t *scale, int fmt, int64_t ro
     return finish();
 }
 
-int sq_gemm_mxfp4(const uint8_t *xq, const uint8_t *x_scale, int x_fmt, const uint8_t *wq,
-                  const uint8_t *w_scale, int64_t M, int64_t N, int64_t K, void *y, int y_dt,
-                  void *stream) {
+int sq_gemm_mxfp4_tile(const uint8_t *xq, const uint8_t *x_scale, int x_fmt, const uint8_t *wq,
+                       const uint8_t *w_scale, int64_t M, int64_t N, int64_t K, void *y, int y_dt,
+                       void *stream, int tile) {
+    if (tile < -1 || tile > 2) return SQ_ERR_ARG;
     if (!valid_dt(y_dt)) return SQ_ERR_DTYPE;
     if (!valid_fmt(x_fmt)) return SQ_ERR_ARG;
     if (bad_rows(M, K) || N < 0 || N > kMaxDim) return SQ_ERR_SHAPE;
     if (M == 0 || N == 0) return SQ_OK;
     if (K == 0) return SQ_ERR_SHAPE;  // an empty inner dimension
+    if (K > 1 << 20) return SQ_ERR_UNSUPPORTED;  // 32-bit offsets inside a tile of 256 rows
     if (!xq || !x_scale || !wq || !w_scale || !y) return SQ_ERR_NULL;
     if (!aligned(xq, 16) || !aligned(wq, 16) || !aligned(x_scale, 4) || !aligned(w_scale, 4) ||
         !aligned(y, esize(y_dt)))
         return SQ_ERR_ALIGN;
-    sq::launch_gemm_mx(xq, x_scale, x_fmt, wq, w_scale, M, N, K, y, y_dt, st(stream));
+    sq::launch_gemm_mx(xq, x_scale, x_fmt, wq, w_scale, M, N, K, y, y_dt, st(stream), tile);
     return finish();
+}
+
+int sq_gemm_mxfp4(const uint8_t *xq, const uint8_t *x_scale, int x_fmt, const uint8_t *wq,
+                  const uint8_t *w_scale, int64_t M, int64_t N, int64_t K, void *y, int y_dt,
+                  void *stream) {
+    return sq_gemm_mxfp4_tile(xq, x_scale, x_fmt, wq, w_scale, M, N, K, y, y_dt, stream, -1);
 }
 
 }  // extern "C"
