@@ -11,11 +11,10 @@
 //   scale of lane (r, g): block g of row r (k = 32 g .. 32 g + 31), both formats
 // Weight rows are the instruction's first operand (rows of its result).
 //
-// Three kernels:
-//  * mx_gemm_dec   M <= 32 (decode), bound by the weight stream.
-//  * mx_gemm_pp    M > 32, K % 128 == 0, K >= 256: both operands through LDS rings
-//                  filled by direct-to-LDS loads.
-//  * mx_gemm_tile  M > 32, other K: staged through registers.
+// Two kernels:
+//  * mx_gemm_dec  M <= 32 (decode), bound by the weight stream; also K < 256.
+//  * mx_gemm_pp   M > 32: both operands through LDS rings filled by
+//                 direct-to-LDS loads.
 #include <type_traits>
 
 #include "mx_device.h"
@@ -28,6 +27,7 @@ struct MxArgs : TileGrid {
     const uint8_t *xq, *xs, *wq, *ws;
     int M, N, K;
     void *y;
+    int y_dt;
     int groups;  // mx_gemm_dec: groups of 16 weight rows a block covers
 };
 
@@ -64,13 +64,6 @@ __device__ __forceinline__ f32x4 mfma16(int4v w, const XFrag<XF> &x, f32x4 acc, 
 }
 
 // ---------------------------------------------------------------- tiled
-
-// The four scale bytes that lane half fh needs for the four 64-element
-// quarters of a stage (blocks 2 q + fh of the row's eight), byte q for
-// quarter q.
-__device__ __forceinline__ int quarter_scales(uint2 s, int fh) {
-    return (int)__builtin_amdgcn_perm(s.y, s.x, fh ? 0x07050301u : 0x06040200u);
-}
 
 // Outputs of a wave's accumulators (32x32 layout: lane l, register v of
 // fragment (i, j) is weight row 8 (v / 4) + 4 (l / 32) + v % 4 of n-fragment
@@ -112,6 +105,18 @@ __device__ __forceinline__ void mx_epilogue(const MxArgs &p,
                 else *reinterpret_cast<uint2 *>(dst) = __builtin_bit_cast(uint2, h);
             }
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // slab written (one wave)
+        if (!vec_y) {
+            // rows that start anywhere: 64 successive outputs of a row a store
+#pragma unroll 8
+            for (int k = 0; k < 32 * (WTN / 64); ++k) {
+                const int r = k / (WTN / 64), nl = (k % (WTN / 64)) * 64 + lane;
+                const int cb = nl * (int)sizeof(T);
+                const T v = *reinterpret_cast<const T *>(
+                    slab + r * RB + (((cb >> 4) ^ ((r / RPW) & (CPR - 1))) << 4) + (cb & 15));
+                const int m = m0 + wm * WTM + j * 32 + r, n = n0 + wn * WTN + nl;
+                if (m < M && n < N) reinterpret_cast<T *>(p.y)[(int64_t)m * N + n] = v;
+            }
+        } else
 #pragma unroll
         for (int k = 0; k < 32 * CPR / 64; ++k) {
             const int c = lane + 64 * k;
@@ -122,7 +127,7 @@ __device__ __forceinline__ void mx_epilogue(const MxArgs &p,
             const int n = n0 + wn * WTN + ch * EPC;
             if (m >= M || n >= N) continue;
             T *yp = reinterpret_cast<T *>(p.y) + (int64_t)m * N + n;
-            if (vec_y && n + EPC <= N) {
+            if (n + EPC <= N) {
                 *reinterpret_cast<uint4 *>(yp) = v;
             } else {
                 T e[EPC];
@@ -151,29 +156,50 @@ __device__ __forceinline__ void mx_sched() {
     }
 }
 
-// K % 128 == 0, K >= 256.  A stage is 256 elements of K: 128 bytes of every weight row,
-// 128 (e2m1) or twice 128 (e4m3, two half tiles) of every activation row, and
-// the rows' eight scale bytes, streamed into a ring of STA LDS stages by
-// direct-to-LDS loads.  Data rows are 128 bytes with chunk c of row r at slot
-// c ^ swz(r).  A stage is consumed as four quarters of 64 elements with
-// ping-pong fragment registers; the scale bytes of a row become one register
-// per fragment and stage, whose byte q the instruction selects in quarter q.
-// Where K % 256 == 128 the last stage is the row's last 256 elements again,
-// of which the first two quarters (added already) are skipped.
-template <int XF, int BM, int BN, int WM, int WN, int STA, int YDT>
-__global__ __launch_bounds__(64 * WM * WN, 1) void mx_gemm_pp(MxArgs p) {
+// K >= 256.  A stage is 256 elements of K: 128 bytes of every weight row and
+// 128 (e2m1) or twice 128 (e4m3, two half tiles) of every activation row,
+// streamed into a ring of STA LDS stages by direct-to-LDS loads, with chunk c
+// of a 128-byte row r at slot c ^ swz(r).  It is consumed as four quarters of
+// 64 elements with ping-pong fragment registers.
+//
+// Which blocks of a stage meet in a quarter is free as long as both operands
+// agree: lane half h takes block 4 h + q in quarter q, so a lane's four scale
+// bytes of a stage are one aligned word of the row's eight, and the
+// instruction selects byte q (e4m3: the chunks that the instruction pairs
+// with blocks q and 4 + q, the file comment).
+//
+// Scales.  A row's bytes of one stage are 8, and a load of those would cost
+// the vector L1 as many line requests as the stage's data (a line per row and
+// stage; measured 47 us against 38 at 256 x 28672 x 7168).  K % 128 == 0
+// (CH > 0): the bytes of CH stages are loaded at a time into an LDS area
+// beside the ring, read into CH words per fragment when their first stage
+// comes up, and the area is refilled during that stage.
+// Other K (CH = 0: a scale row starts at any byte, which direct-to-LDS loads
+// cannot fetch): each thread loads one row's eight bytes with the stage's
+// data and writes them to LDS where the stage is waited for.
+//
+// K % 256 != 0: the last stage is the row's last 256 elements again, and the
+// weights of its first blocks, which are added already, count as zero.
+template <int XF, int BM, int BN, int WM, int WN, int STA, int CH>
+__global__ __launch_bounds__(64 * WM * WN, 2) void mx_gemm_pp(MxArgs p) {
+    constexpr bool REGS = CH == 0;
     constexpr int NW = WM * WN, XH = XF == E4M3 ? 2 : 1;
     constexpr int WTM = BM / WM, WTN = BN / WN;
     constexpr int FM = WTM / 32, FN = WTN / 32;
     constexpr int LX = BM * XH / (8 * NW), LW = BN / (8 * NW);  // 1 KB loads per wave and stage
-    constexpr int LS = (BM + BN + 32 * NW - 1) / (32 * NW);     // 256 B scale loads
-    constexpr int L = LX + LW + LS;
-    constexpr int SX = BM * 128 * XH, SW = BN * 128, SS = LS * NW * 256;
-    constexpr int STG = SX + SW + SS;
-    static_assert(FM >= 1 && FN >= 1 && LX >= 1 && LW >= 1 && LS >= 1 && LS <= 4, "tile");
-    static_assert(STA >= 2 && STA * L < 64, "vmcnt range");
-    static_assert(NW * 32 * WTN * (int)sizeof(typename OutT<YDT>::T) <= STA * STG, "slabs");
-    __shared__ __attribute__((aligned(1024))) uint8_t smem[STA * STG];
+    constexpr int RPS = REGS ? 1 : 32 / (REGS ? 1 : CH);         // rows per 256 B scale load
+    constexpr int LS = REGS ? 0 : (BM + BN) / (RPS * NW);        // scale loads per CH stages
+    constexpr int L = LX + LW;
+    constexpr int SX = BM * 128 * XH, SW = BN * 128, STG = SX + SW;
+    constexpr int SS = (BM + BN) * 8 * (REGS ? 2 : CH);
+    static_assert(FM >= 1 && FN >= 1 && LX >= 1 && LW >= 1, "tile");
+    static_assert(CH == 0 || CH == 2 || CH == 4, "stages per scale load");
+    static_assert(REGS || (LS * RPS * NW == BM + BN && BM % RPS == 0 && STA <= CH + 1), "scale loads");
+    static_assert(STA >= 2 && STA * L + 2 * LS < 64, "vmcnt range");
+    static_assert(!REGS || (BM + BN == 64 * NW && STA == 2), "one scale row per thread");
+    static_assert(NW * 32 * WTN * 4 <= STA * STG, "slabs");
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[STA * STG + SS];
+    uint8_t *const sscale = smem + STA * STG;
 
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int wm = wave / WN, wn = wave % WN;
@@ -182,12 +208,12 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void mx_gemm_pp(MxArgs p) {
     const int m0 = tile_m * BM, n0 = tile_n * BN;
     const int M = p.M, N = p.N, K = p.K;
     const int KB = K >> 5;
-    const int nk = (K + 255) >> 8;
-    const bool half = (K & 128) != 0;  // the last stage adds 128 elements
+    const int nk = (KB + 7) >> 3;
+    const int skip = nk * 8 - KB;  // blocks of the last stage that are added already
 
     // This wave's loads: offsets of its lanes from the tile's first row (rows
     // past the edge read a valid row, whose outputs are never stored).
-    uint32_t x_off[LX], w_off[LW], s_off[LS];
+    uint32_t x_off[LX], w_off[LW];
     const int mtop = M - 1 - m0, ntop = N - 1 - n0;
 #pragma unroll
     for (int j = 0; j < LX; ++j) {
@@ -202,56 +228,111 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void mx_gemm_pp(MxArgs p) {
         const int c = (lane & 7) ^ swz(row);
         w_off[j] = (uint32_t)(row < ntop ? row : ntop) * (uint32_t)(K / 2) + c * 16 + dma_bias<16>(j);
     }
-    // Scale rows: the tile's activation rows (load instructions below LSX of
-    // the block's LS NW), then its weight rows; those past both repeat the last.
-    constexpr int LSX = BM / 32;
     const uint8_t *xs0 = p.xs + (int64_t)m0 * KB, *ws0 = p.ws + (int64_t)n0 * KB;
-#pragma unroll
-    for (int j = 0; j < LS; ++j) {
-        const int i = wave * LS + j;
-        int row = (i < LSX ? i : i - LSX) * 32 + (lane >> 1);
-        const int top = i < LSX ? mtop : ntop < BN - 1 ? ntop : BN - 1;
-        row = row < top ? row : top;
-        s_off[j] = (uint32_t)row * (uint32_t)KB + 4 * (lane & 1) + dma_bias<4>(0);
-    }
     const uint32_t waveu = (uint32_t)__builtin_amdgcn_readfirstlane(wave);
     const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_void_t *)smem;
     const uint8_t *xq0 = p.xq + (int64_t)m0 * (K * (int64_t)XH / 2), *wq0 = p.wq + (int64_t)n0 * (K / 2);
-    auto issue = [&](int s) {  // stage s < nk
+    const uint8_t *s_row = nullptr;  // REGS: this thread's scale row
+    if constexpr (REGS) {
+        s_row = tid < BM ? xs0 + (int64_t)(tid < mtop ? tid : mtop) * KB
+                         : ws0 + (int64_t)(tid - BM < ntop ? tid - BM : ntop) * KB;
+    }
+    uint2 rs = make_uint2(0, 0);
+    auto issue = [&](int s) __attribute__((always_inline)) {  // stage s < nk
         const uint32_t base = lds0 + (uint32_t)((s % STA) * STG);
         const int b0 = s * 8 < KB - 8 ? s * 8 : KB - 8;  // the stage's first block
         lds_dma_based<LX, 16, false>(x_off, xq0 + b0 * (16 * XH), base + waveu * (LX * 1024u));
         lds_dma_based<LW, 16, false>(w_off, wq0 + b0 * 16, base + SX + waveu * (LW * 1024u));
+        if constexpr (REGS) __builtin_memcpy(&rs, s_row + b0, 8);
+    };
+    // CH > 0: the scales of stages CH c .. CH c + CH - 1.  Load i of the block
+    // covers RPS rows of 2 CH words, activation rows first; words past a row's
+    // end repeat its last.  Word d of a row sits at d ^ scale_swz(row), which
+    // spreads the words that a wave reads (one per row and lane half) over
+    // all banks.
+    auto scale_swz = [](int row) { return 2 * ((row / RPS) & (32 / RPS - 1)); };
+    auto issue_scales = [&](int c) __attribute__((always_inline)) {
+        if constexpr (!REGS) {
+            // (opaque, so that the offsets below are formed here, every CH
+            // stages, and not kept in registers through the loop)
+            int ln = lane;
+            asm volatile("" : "+v"(ln));
 #pragma unroll
-        for (int j = 0; j < LS; ++j)
-            lds_dma_based<1, 4, false>(s_off + j, ((int)(waveu * LS) + j < LSX ? xs0 : ws0) + b0,
-                                       base + SX + SW + (waveu * LS + j) * 256u);
+            for (int j = 0; j < LS; ++j) {
+                const int i = (int)waveu * LS + j;
+                const bool is_x = i < BM / RPS;
+                const int r = (is_x ? i : i - BM / RPS) * RPS + ln / (2 * CH), top = is_x ? mtop : ntop;
+                int b = 8 * CH * c + 4 * ((ln & (2 * CH - 1)) ^ scale_swz(i * RPS));
+                b = b < KB - 4 ? b : KB - 4;
+                const uint32_t off = (uint32_t)(r < top ? r : top) * (uint32_t)KB + (uint32_t)b + dma_bias<4>(0);
+                lds_dma_based<1, 4, false>(&off, is_x ? xs0 : ws0, lds0 + (uint32_t)(STA * STG) + i * 256u);
+            }
+        }
     };
 
     const int fr = lane & 31, fh = lane >> 5;
     const int fsw = swz(fr);  // fragment bases are multiples of 32 rows
-    auto read_frags = [&](int s, int q, XFrag<XF> (&xf)[FM], int4v (&wf)[FN]) {
-        const uint8_t *xb = smem + (s % STA) * STG + (XF == E4M3 ? (q >> 1) * (BM * 128) : 0);
+    auto read_frags = [&](int s, int q, XFrag<XF> (&xf)[FM],
+                          int4v (&wf)[FN]) __attribute__((always_inline)) {
+        const uint8_t *xb = smem + (s % STA) * STG;
         const uint8_t *wb = smem + (s % STA) * STG + SX;
 #pragma unroll
         for (int f = 0; f < FM; ++f)
 #pragma unroll
             for (int c = 0; c < XH; ++c) {
-                const int ch = XF == E4M3 ? 4 * (q & 1) + 2 * c + fh : 2 * q + fh;
+                // e4m3: chunk 2 q + h of block q's half tile, then of 4 + q's
+                const int ch = XF == E4M3 ? 2 * q + fh : 4 * fh + q;
                 xf[f].c[c] = *reinterpret_cast<const int4v *>(
-                    xb + (wm * WTM + f * 32 + fr) * 128 + ((ch ^ fsw) << 4));
+                    xb + c * (BM * 128) + (wm * WTM + f * 32 + fr) * 128 + ((ch ^ fsw) << 4));
             }
 #pragma unroll
         for (int f = 0; f < FN; ++f)
             wf[f] = *reinterpret_cast<const int4v *>(wb + (wn * WTN + f * 32 + fr) * 128 +
-                                                     (((2 * q + fh) ^ fsw) << 4));
+                                                     (((4 * fh + q) ^ fsw) << 4));
     };
-    auto read_scales = [&](int s, uint2 (&sx)[FM], uint2 (&sw)[FN]) {
-        const uint2 *sb = reinterpret_cast<const uint2 *>(smem + (s % STA) * STG + SX + SW);
+    // A fragment's scale words: [0] the next stage's, then (CH > 0) those of
+    // the stages after it that the area held when it was read.
+    constexpr int SN = REGS ? 1 : CH;
+    uint32_t nx[FM][SN], nw[FN][SN];
+    auto read_scales = [&](int s) __attribute__((always_inline)) {  // stage s becomes the next
+        if constexpr (REGS) {
+            const uint8_t *b = sscale + (s & 1) * ((BM + BN) * 8) + 4 * fh;
 #pragma unroll
-        for (int f = 0; f < FM; ++f) sx[f] = sb[wm * WTM + f * 32 + fr];
+            for (int f = 0; f < FM; ++f)
+                nx[f][0] = *reinterpret_cast<const uint32_t *>(b + (wm * WTM + f * 32 + fr) * 8);
 #pragma unroll
-        for (int f = 0; f < FN; ++f) sw[f] = sb[BM + wn * WTN + f * 32 + fr];
+            for (int f = 0; f < FN; ++f)
+                nw[f][0] = *reinterpret_cast<const uint32_t *>(b + (BM + wn * WTN + f * 32 + fr) * 8);
+        } else if ((s & (SN - 1)) == 0) {
+            const uint8_t *at[SN];
+            int row = fr;
+            asm volatile("" : "+v"(row));  // (as in issue_scales)
+#pragma unroll
+            for (int i = 0; i < SN; ++i) {
+                // (the last stage of K % 256 == 128 has its new blocks in its
+                // area's first word, and they are the upper lane half's)
+                const int d = 2 * i + (skip && s + i == nk - 1 ? 0 : fh);
+                at[i] = sscale + row * (8 * SN) + 4 * (d ^ scale_swz(row));
+            }
+#pragma unroll
+            for (int f = 0; f < FM; ++f)
+#pragma unroll
+                for (int i = 0; i < SN; ++i)
+                    nx[f][i] = *reinterpret_cast<const uint32_t *>(at[i] + (wm * WTM + f * 32) * (8 * SN));
+#pragma unroll
+            for (int f = 0; f < FN; ++f)
+#pragma unroll
+                for (int i = 0; i < SN; ++i)
+                    nw[f][i] = *reinterpret_cast<const uint32_t *>(at[i] + (BM + wn * WTN + f * 32) * (8 * SN));
+        } else {
+#pragma unroll
+            for (int i = 0; i + 1 < SN; ++i) {
+#pragma unroll
+                for (int f = 0; f < FM; ++f) nx[f][i] = nx[f][i + 1];
+#pragma unroll
+                for (int f = 0; f < FN; ++f) nw[f][i] = nw[f][i + 1];
+            }
+        }
     };
 
     f32x16 acc[FN][FM];
@@ -262,7 +343,8 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void mx_gemm_pp(MxArgs p) {
 #pragma unroll
             for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
     int cx[FM], cw[FN];  // this stage's scales
-    auto mma = [&](auto qc, const XFrag<XF> (&xf)[FM], const int4v (&wf)[FN]) {
+    auto mma = [&](auto qc, const XFrag<XF> (&xf)[FM],
+                   const int4v (&wf)[FN]) __attribute__((always_inline)) {
         constexpr int Q = decltype(qc)::value;
 #pragma unroll
         for (int i = 0; i < FN; ++i)
@@ -270,11 +352,15 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void mx_gemm_pp(MxArgs p) {
             for (int j = 0; j < FM; ++j)
                 acc[i][j] = mfma32<XF, Q>(wf[i], xf[j], acc[i][j], cw[i], cx[j]);
     };
-    auto take_scales = [&](const uint2 (&sx)[FM], const uint2 (&sw)[FN]) {
+    auto take_scales = [&]() {
 #pragma unroll
-        for (int f = 0; f < FM; ++f) cx[f] = quarter_scales(sx[f], fh);
+        for (int f = 0; f < FM; ++f) cx[f] = (int)nx[f][0];
 #pragma unroll
-        for (int f = 0; f < FN; ++f) cw[f] = quarter_scales(sw[f], fh);
+        for (int f = 0; f < FN; ++f) cw[f] = (int)nw[f][0];
+    };
+    // Where stage s has landed in this wave: its scale rows go to LDS too.
+    auto publish_scales = [&](int s) {
+        if constexpr (REGS) *reinterpret_cast<uint2 *>(sscale + (s & 1) * ((BM + BN) * 8) + tid * 8) = rs;
     };
     constexpr std::integral_constant<int, 0> q0;
     constexpr std::integral_constant<int, 1> q1;
@@ -282,221 +368,100 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void mx_gemm_pp(MxArgs p) {
     constexpr std::integral_constant<int, 3> q3;
     constexpr int RQ = FM * XH + FN, MQ = FM * FN;
 
+    if constexpr (!REGS) issue_scales(0);
+    issue(0);
+    publish_scales(0);  // (waits for its row; the ring is empty anyway)
 #pragma unroll
-    for (int s = 0; s < STA; ++s)
+    for (int s = 1; s < STA; ++s)
         if (s < nk) issue(s);
-    wait_stages<STA - 1, L>((nk < STA ? nk : STA) - 1);  // stage 0 landed
+    wait_stages<STA - 1, L + (REGS ? 1 : 0)>((nk < STA ? nk : STA) - 1);  // stage 0 landed
     lds_barrier();
     XFrag<XF> xa[FM], xb[FM];
     int4v wa[FN], wb[FN];
-    uint2 nx[FM], nw[FN];
-    read_scales(0, nx, nw);
+    read_scales(0);
     read_frags(0, 0, xa, wa);
+    // A stage: its last quarter multiplies behind the barrier, while the next
+    // stage's first fragments are read and stage kt + STA's loads issue.  The
+    // empty asm keeps the sums of the first three quarters before the barrier:
+    // their next use is behind a branch (the scales), and the compiler would
+    // move all of their multiplies there, past every wait (measured: the matrix
+    // cores 26 % busy).  The scale area is refilled in the first of its CH
+    // stages, when every wave has read it.
+    auto stage = [&](int kt, auto issue_c) __attribute__((always_inline)) {
+        constexpr bool ISSUE = decltype(issue_c)::value;
+        take_scales();
+        read_frags(kt, 1, xb, wb);
+        mma(q0, xa, wa);
+        mx_sched<MQ, RQ, 0>();
+        read_frags(kt, 2, xa, wa);
+        mma(q1, xb, wb);
+        mx_sched<MQ, RQ, 0>();
+        read_frags(kt, 3, xb, wb);
+        mma(q2, xa, wa);
+        mx_sched<MQ, RQ, 0>();
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+#pragma unroll
+            for (int j = 0; j < FM; ++j) asm volatile("" : "+v"(acc[i][j]));
+        if constexpr (ISSUE) wait_vmcnt<(STA - 2) * L>();  // stage kt + 1 landed
+        else wait_stages<STA - 2, L>(nk - kt - 2);
+        publish_scales(kt + 1);
+        lds_barrier();  // every wave has read stage kt: its slot is free
+        read_scales(kt + 1);
+        if constexpr (!REGS)
+            if ((kt & (SN - 1)) == 0 && kt + SN < nk) issue_scales(kt / SN + 1);
+        read_frags(kt + 1, 0, xa, wa);
+        if constexpr (ISSUE) issue(kt + STA);
+        mma(q3, xb, wb);
+        mx_sched<MQ, RQ, ISSUE ? L : 0>();
+    };
     int kt = 0;
-    for (; kt + STA < nk; ++kt) {
-        take_scales(nx, nw);
+    for (; kt + STA < nk; ++kt) stage(kt, std::true_type{});
+    for (; kt + 1 < nk; ++kt) stage(kt, std::false_type{});  // nothing left to issue
+    {  // the last stage: the weights of blocks that are added already are zero
+        auto masked = [&](int q, int4v (&wf)[FN]) __attribute__((always_inline)) {
+#pragma unroll
+            for (int f = 0; f < FN; ++f) wf[f] = 4 * fh + q >= skip ? wf[f] : int4v{0, 0, 0, 0};
+        };
+        take_scales();
         read_frags(kt, 1, xb, wb);
+        masked(0, wa);
         mma(q0, xa, wa);
-        mx_sched<MQ, RQ, 0>();
         read_frags(kt, 2, xa, wa);
+        masked(1, wb);
         mma(q1, xb, wb);
-        mx_sched<MQ, RQ, 0>();
         read_frags(kt, 3, xb, wb);
+        masked(2, wa);
         mma(q2, xa, wa);
-        mx_sched<MQ, RQ, 0>();
-        wait_vmcnt<(STA - 2) * L>();  // stage kt + 1 landed
-        lds_barrier();                // every wave has read stage kt: its slot is free
-        read_scales(kt + 1, nx, nw);
-        read_frags(kt + 1, 0, xa, wa);
-        issue(kt + STA);
-        mma(q3, xb, wb);
-        mx_sched<MQ, RQ + FM + FN, L>();
-    }
-    const int nfull = half ? nk - 1 : nk;
-    for (; kt < nfull; ++kt) {  // nothing left to issue
-        take_scales(nx, nw);
-        read_frags(kt, 1, xb, wb);
-        mma(q0, xa, wa);
-        mx_sched<MQ, RQ, 0>();
-        read_frags(kt, 2, xa, wa);
-        mma(q1, xb, wb);
-        mx_sched<MQ, RQ, 0>();
-        read_frags(kt, 3, xb, wb);
-        mma(q2, xa, wa);
-        mx_sched<MQ, RQ, 0>();
-        wait_stages<STA - 2, L>(nk - kt - 2);  // stage kt + 1 landed (if any)
-        lds_barrier();
-        read_scales(kt + 1, nx, nw);  // past the last stage: never used
-        read_frags(kt + 1, 0, xa, wa);
-        mma(q3, xb, wb);
-    }
-    if (half) {
-        take_scales(nx, nw);
-        read_frags(kt, 2, xa, wa);
-        read_frags(kt, 3, xb, wb);
-        mma(q2, xa, wa);
+        masked(3, wb);
         mma(q3, xb, wb);
     }
     wait_vmcnt<0>();
     __syncthreads();  // the ring becomes the output slabs
-    mx_epilogue<BM, BN, WM, WN, YDT>(p, acc, smem, m0, n0);
-}
-
-// Any K (a multiple of 32): 128 x 128 tiles of four waves, a stage of 256
-// elements of K loaded into registers while the previous one multiplies, then
-// written to one of two LDS buffers in mx_gemm_pp's layout.  Chunks past K
-// are zero with scale 1.  (Scale rows of K / 32 bytes start at any byte here,
-// which direct-to-LDS loads cannot fetch.)
-template <int XF, int YDT>
-__global__ __launch_bounds__(256, 1) void mx_gemm_tile(MxArgs p) {
-    constexpr int BM = 128, BN = 128, WM = 2, WN = 2, XH = XF == E4M3 ? 2 : 1;
-    constexpr int WTM = BM / WM, WTN = BN / WN, FM = WTM / 32, FN = WTN / 32;
-    constexpr int TX = BM * 8 * XH / 256, TW = BN * 8 / 256;  // chunks per thread and stage
-    constexpr int SX = BM * 128 * XH, SW = BN * 128, SS = (BM + BN) * 8, STG = SX + SW + SS;
-    static_assert(BM + BN == 256, "one scale row per thread");
-    __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * STG];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int wm = wave / WN, wn = wave % WN;
-    int tile_m, tile_n;
-    tile_of(p, blockIdx.x, tile_m, tile_n);
-    const int m0 = tile_m * BM, n0 = tile_n * BN;
-    const int M = p.M, N = p.N, K = p.K, KB = K >> 5;
-    const int nk = (K + 255) >> 8;
-
-    const uint8_t *x_src[TX], *w_src[TW], *s_src;
-    int x_chunk[TX], w_chunk[TW], x_lds[TX], w_lds[TW];
-#pragma unroll
-    for (int j = 0; j < TX; ++j) {
-        const int i = tid + 256 * j, hh = i / (BM * 8), row = (i / 8) % BM, c = i & 7;
-        const int64_t m = m0 + row < M ? m0 + row : M - 1;
-        x_chunk[j] = hh * 8 + c;
-        x_src[j] = p.xq + m * KB * (16 * XH) + x_chunk[j] * 16;
-        x_lds[j] = hh * (BM * 128) + row * 128 + ((c ^ swz(row)) << 4);
-    }
-#pragma unroll
-    for (int j = 0; j < TW; ++j) {
-        const int i = tid + 256 * j, row = i / 8, c = i & 7;
-        const int64_t n = n0 + row < N ? n0 + row : N - 1;
-        w_chunk[j] = c;
-        w_src[j] = p.wq + n * KB * 16 + c * 16;
-        w_lds[j] = SX + row * 128 + ((c ^ swz(row)) << 4);
-    }
-    {
-        const int64_t m = m0 + tid < M ? m0 + tid : M - 1;
-        const int64_t n = n0 + tid - BM < N ? n0 + tid - BM : N - 1;
-        s_src = tid < BM ? p.xs + m * KB : p.ws + n * KB;
-    }
-    uint4 rx[TX], rw[TW];
-    uint2 rs;
-    // (chunks past K load the row's first chunk and are zeroed after: a load
-    // under a lane-dependent condition would wait for the earlier ones)
-    auto load = [&](int s) {
-#pragma unroll
-        for (int j = 0; j < TX; ++j) {
-            const bool in = s * 8 * XH + x_chunk[j] < KB * XH;
-            const uint4 v = *reinterpret_cast<const uint4 *>(
-                x_src[j] + (in ? s * 128 * XH : -16 * x_chunk[j]));
-            rx[j] = in ? v : make_uint4(0, 0, 0, 0);
-        }
-#pragma unroll
-        for (int j = 0; j < TW; ++j) {
-            const bool in = s * 8 + w_chunk[j] < KB;
-            const uint4 v =
-                *reinterpret_cast<const uint4 *>(w_src[j] + (in ? s * 128 : -16 * w_chunk[j]));
-            rw[j] = in ? v : make_uint4(0, 0, 0, 0);
-        }
-        if (s * 8 + 8 <= KB) {
-            __builtin_memcpy(&rs, s_src + s * 8, 8);
-        } else {
-            uint8_t b[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint8_t v = s_src[s * 8 + i < KB ? s * 8 + i : 0];
-                b[i] = s * 8 + i < KB ? v : 127;
-            }
-            __builtin_memcpy(&rs, b, 8);
-        }
-    };
-    auto store = [&](int buf) {
-        uint8_t *base = smem + buf * STG;
-#pragma unroll
-        for (int j = 0; j < TX; ++j) *reinterpret_cast<uint4 *>(base + x_lds[j]) = rx[j];
-#pragma unroll
-        for (int j = 0; j < TW; ++j) *reinterpret_cast<uint4 *>(base + w_lds[j]) = rw[j];
-        *reinterpret_cast<uint2 *>(base + SX + SW + tid * 8) = rs;
-    };
-
-    const int fr = lane & 31, fh = lane >> 5, fsw = swz(fr);
-    f32x16 acc[FN][FM];
-#pragma unroll
-    for (int i = 0; i < FN; ++i)
-#pragma unroll
-        for (int j = 0; j < FM; ++j)
-#pragma unroll
-            for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
-
-    load(0);
-    store(0);
-    __syncthreads();
-    for (int kt = 0; kt < nk; ++kt) {
-        if (kt + 1 < nk) load(kt + 1);
-        const uint8_t *base = smem + (kt & 1) * STG;
-        const uint2 *sb = reinterpret_cast<const uint2 *>(base + SX + SW);
-        int cx[FM], cw[FN];
-#pragma unroll
-        for (int f = 0; f < FM; ++f) cx[f] = quarter_scales(sb[wm * WTM + f * 32 + fr], fh);
-#pragma unroll
-        for (int f = 0; f < FN; ++f) cw[f] = quarter_scales(sb[BM + wn * WTN + f * 32 + fr], fh);
-        auto quarter = [&](auto qc) {
-            constexpr int Q = decltype(qc)::value;
-            XFrag<XF> xf[FM];
-            int4v wf[FN];
-#pragma unroll
-            for (int f = 0; f < FM; ++f)
-#pragma unroll
-                for (int c = 0; c < XH; ++c) {
-                    const int ch = XF == E4M3 ? 4 * (Q & 1) + 2 * c + fh : 2 * Q + fh;
-                    xf[f].c[c] = *reinterpret_cast<const int4v *>(
-                        base + (XF == E4M3 ? (Q >> 1) * (BM * 128) : 0) +
-                        (wm * WTM + f * 32 + fr) * 128 + ((ch ^ fsw) << 4));
-                }
-#pragma unroll
-            for (int f = 0; f < FN; ++f)
-                wf[f] = *reinterpret_cast<const int4v *>(
-                    base + SX + (wn * WTN + f * 32 + fr) * 128 + (((2 * Q + fh) ^ fsw) << 4));
-#pragma unroll
-            for (int i = 0; i < FN; ++i)
-#pragma unroll
-                for (int j = 0; j < FM; ++j)
-                    acc[i][j] = mfma32<XF, Q>(wf[i], xf[j], acc[i][j], cw[i], cx[j]);
-        };
-        quarter(std::integral_constant<int, 0>{});
-        quarter(std::integral_constant<int, 1>{});
-        quarter(std::integral_constant<int, 2>{});
-        quarter(std::integral_constant<int, 3>{});
-        if (kt + 1 < nk) store((kt + 1) & 1);
-        __syncthreads();
-    }
-    mx_epilogue<BM, BN, WM, WN, YDT>(p, acc, smem, m0, n0);
+    if (p.y_dt == F32) mx_epilogue<BM, BN, WM, WN, F32>(p, acc, smem, m0, n0);
+    else if (p.y_dt == F16) mx_epilogue<BM, BN, WM, WN, F16>(p, acc, smem, m0, n0);
+    else mx_epilogue<BM, BN, WM, WN, BF16>(p, acc, smem, m0, n0);
 }
 
 // ---------------------------------------------------------------- decode
 
-// M <= 32.  Bound by the weight stream, so a block of eight waves reads each
-// byte of its weight rows once and everything else is kept small: the waves
-// split K, each holds its part of the 16 FT activation rows in registers for
-// the whole kernel (read once per block), and streams its part of the weight
-// rows, a group of 16 rows a stage, through a private ring of S LDS stages by
-// direct-to-LDS loads.  No barrier until the end, where the waves' sums of
-// every group are added through LDS in wave order.
+// M <= 32, or K < 256 in slabs of 32 tokens (blockIdx.y).  Bound by the weight
+// stream, so a block of eight waves reads each byte of its weight rows once
+// and everything else is kept small: the waves split K, each holds its part of
+// the 16 FT activation rows in registers for all of the block's weight rows,
+// and streams its part of these, a group of 16 rows at a time, through a
+// private ring of S LDS stages by direct-to-LDS loads.  No barrier until the
+// end, where the waves' sums are added through LDS in wave order.
 //
-// A wave's part of K is a window of 128 SPW elements (64 SPW bytes of a
-// weight row); windows repeat every 8 * 128 SPW elements for a longer K.
-// Which blocks of the window meet in an instruction is free as long as both
-// operands agree: lane group g takes the SPW successive blocks SPW g + j in
-// steps j, so its scale bytes are SPW successive bytes of the row (one load,
-// byte j selected by the instruction), and the 16-byte e4m3 chunks are those
-// that the instruction pairs with these blocks (the file comment).
+// A stage is a window of 128 SPW elements (64 SPW bytes) of a group's rows.
+// Wave w has windows w, w + 8, ..., and holds the activations of WPW of them at
+// a time: the eight waves read successive bytes of a row together (with two
+// neighbouring windows a wave instead, the waves in step read every other
+// 256 bytes: 27 us against 23 at M = 1, N = 28672, K = 8192).  Which blocks of a window meet in an instruction is free as
+// long as both operands agree: lane group g takes the SPW successive blocks
+// SPW g + j in steps j, so its scale bytes are SPW successive bytes of the row
+// (one load, byte j selected by the instruction), and the 16-byte e4m3 chunks
+// are those that the instruction pairs with these blocks (the file comment).
 //
 // Blocks past K: their activation chunks are zero and their scales 1; the
 // weight lanes re-read the row's first chunk (e2m1 codes are all finite).
@@ -507,24 +472,30 @@ __device__ __forceinline__ int dec_chunk_swz(int r) {
     return SPW >= 4 ? r : SPW == 2 ? (r >> 1) & 7 : (r >> 2) & 3;
 }
 
-// SPW successive scale bytes from byte b of a row of KB, 127 past its end,
-// byte j of word j / 4 for step j.
+// SPW successive scale bytes from byte b of a row of KB, 127 past its end, in
+// the low bytes.
 template <int SPW>
-__device__ __forceinline__ void dec_scales(const uint8_t *row, int b, int KB, uint32_t (&s)[(SPW + 3) / 4]) {
+__device__ __forceinline__ uint32_t dec_scales(const uint8_t *row, int b, int KB) {
+    uint32_t s = 0x7f7f7f7fu;
     if (b + SPW <= KB) {
-        if constexpr (SPW < 4) s[0] = 0;
-        __builtin_memcpy(s, row + b, SPW);
+        __builtin_memcpy(&s, row + b, SPW);
     } else {
 #pragma unroll
-        for (int w = 0; w < (SPW + 3) / 4; ++w) s[w] = 0x7f7f7f7fu;
-#pragma unroll
         for (int j = 0; j < SPW; ++j)
-            if (b + j < KB)
-                s[j / 4] = (s[j / 4] & ~(0xffu << (8 * (j & 3)))) | ((uint32_t)row[b + j] << (8 * (j & 3)));
+            if (b + j < KB) s = (s & ~(0xffu << (8 * j))) | ((uint32_t)row[b + j] << (8 * j));
     }
+    return s;
 }
 
-template <int XF, int FT, int SPW, int NG, int S, int YDT>
+// Where a wave's sums of a fragment lie in LDS for the join: lane (ri, rg)'s
+// four (one token, four successive weight rows) at 16-byte slot
+// 16 rg + (ri ^ (4 rg + group)), so that both the lanes that write and the
+// threads that read successive rows of a token spread over the banks.
+__device__ __forceinline__ int join_slot(int ri, int rg, int group) {
+    return 16 * rg + (ri ^ ((4 * rg + group) & 15));
+}
+
+template <int XF, int FT, int SPW, int WPW, int NG, int S, int YDT>
 __global__ __launch_bounds__(512, 1) void mx_gemm_dec(MxArgs p) {
     constexpr int NW = 8, XH = XF == E4M3 ? 2 : 1;
     constexpr int SLOT = SPW * 1024;          // one stage: 16 rows of 64 SPW bytes
@@ -533,21 +504,24 @@ __global__ __launch_bounds__(512, 1) void mx_gemm_dec(MxArgs p) {
     constexpr int LDSB = NW * (RING > RED ? RING : RED);
     constexpr int CPR = 4 * SPW;              // 16-byte chunks per row and stage
     constexpr int RPI = 64 / CPR;             // rows per 1 KB load
-    constexpr int SWORDS = (SPW + 3) / 4;
-    static_assert(RPI >= 1 && RPI * SPW == 16, "a load covers whole rows");
+    constexpr int WB = 4 * SPW;               // blocks per window
+    static_assert(SPW == 1 || SPW == 2 || SPW == 4, "one scale word per window");
     static_assert(S >= 2 && S * SPW < 64 && LDSB <= 160 * 1024, "ring");
     __shared__ __attribute__((aligned(1024))) uint8_t smem[LDSB];
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int M = p.M, N = p.N, K = p.K, KB = K >> 5;
+    const int N = p.N, K = p.K, KB = K >> 5;
+    const int64_t ms = (int64_t)blockIdx.y * (16 * FT);  // the slab's first token
+    const int M = p.M - ms < 16 * FT ? (int)(p.M - ms) : 16 * FT;
     const int ng = p.groups;
     const int n0 = blockIdx.x * ng * 16;
     const int ri = lane & 15, rg = lane >> 4;  // operand row and lane group
-    constexpr int WB = 4 * SPW;                // blocks per window
-    // windows of this wave: wave, wave + 8, ... below nwin
+    const uint8_t *xs = p.xs + ms * KB, *xq = p.xq + ms * KB * (16 * XH);
+    // this wave's windows: wave, wave + 8, ..., WPW of them a pass (those past
+    // K are all zero)
     const int nwin = (KB + WB - 1) / WB;
-    const int mine = nwin > wave ? (nwin - wave + NW - 1) / NW : 0;
+    const int passes = nwin > wave ? (nwin - wave + NW * WPW - 1) / (NW * WPW) : 0;
 
     // Loader: in load i lane l fetches row i RPI + l / CPR of the group, chunk
     // (l % CPR) ^ f(row) of the window.
@@ -555,23 +529,31 @@ __global__ __launch_bounds__(512, 1) void mx_gemm_dec(MxArgs p) {
     const int lrow = lane / CPR, lpos = lane % CPR;
     const int ntop = N - 1 - n0;
     const uint8_t *wq0 = p.wq + (int64_t)n0 * KB * 16;
-    auto issue = [&](int t) {  // stage t: window wave + 8 (t / ng), group t % ng
-        const int win = wave + NW * (t / ng), grp = t % ng;
-        const uint32_t slot = ring + (uint32_t)((t % S) * SLOT);
+    int iw = 0, ig = 0, ip = 0, islot = 0;  // window, group, pass and slot of the next issue
+    auto issue = [&]() {
+        const int b0 = ((ip * WPW + iw) * NW + wave) * WB;
         uint32_t off[SPW];
 #pragma unroll
         for (int i = 0; i < SPW; ++i) {
-            const int r = grp * 16 + i * RPI + lrow;
-            const int c = win * WB + (lpos ^ dec_chunk_swz<SPW>((i * RPI + lrow) & 15));
+            const int r = ig * 16 + i * RPI + lrow;
+            const int c = b0 + (lpos ^ dec_chunk_swz<SPW>((i * RPI + lrow) & 15));
             off[i] = ((uint32_t)(r < ntop ? r : ntop) * (uint32_t)KB + (c < KB ? c : 0)) * 16u +
                      dma_bias<16>(i);
         }
-        lds_dma_based<SPW, 16, true>(off, wq0, slot);
+        lds_dma_based<SPW, 16, true>(off, wq0, ring + (uint32_t)(islot * SLOT));
+        islot = islot + 1 == S ? 0 : islot + 1;
+        if (++iw == WPW) {
+            iw = 0;
+            if (++ig == ng) {
+                ig = 0;
+                ++ip;
+            }
+        }
     };
-    const int nst = mine * ng;
+    const int nst = passes * ng * WPW;
 #pragma unroll
     for (int t = 0; t < S - 1; ++t)
-        if (t < nst) issue(t);
+        if (t < nst) issue();
 
     f32x4 acc[NG][FT];
 #pragma unroll
@@ -581,67 +563,73 @@ __global__ __launch_bounds__(512, 1) void mx_gemm_dec(MxArgs p) {
     const uint8_t *rd = smem + wave * RING + ri * (64 * SPW);
     const int fsw = dec_chunk_swz<SPW>(ri);
 
-    int t = 0;
-    for (int w = 0; w < mine; ++w) {
-        const int b0 = (wave + NW * w) * WB;  // the window's first block
-        // this window's activations and every group's weight scales
-        XFrag<XF> xf[FT][SPW];
-        uint32_t sx[FT][SWORDS], sw[NG][SWORDS];
+    int t = 0, slot = 0;
+    for (int pass = 0; pass < passes; ++pass) {
+        // this pass's activations and every group's weight scales
+        XFrag<XF> xf[FT][WPW][SPW];
+        uint32_t sx[FT][WPW], sw[NG][WPW];
 #pragma unroll
         for (int f = 0; f < FT; ++f) {
             const int m = f * 16 + ri < M ? f * 16 + ri : M - 1;
-            dec_scales<SPW>(p.xs + (int64_t)m * KB, b0 + SPW * rg, KB, sx[f]);
-            const uint8_t *row = p.xq + (int64_t)m * KB * (16 * XH);
+            const uint8_t *row = xq + (int64_t)m * KB * (16 * XH);
 #pragma unroll
-            for (int j = 0; j < SPW; ++j)
+            for (int v = 0; v < WPW; ++v) {
+                const int bw = ((pass * WPW + v) * NW + wave) * WB;
+                sx[f][v] = dec_scales<SPW>(xs + (int64_t)m * KB, bw + SPW * rg, KB);
 #pragma unroll
-                for (int c = 0; c < XH; ++c) {
-                    const int b = XF == E4M3 ? b0 + SPW * (2 * c + (rg >> 1)) + j : b0 + SPW * rg + j;
-                    const int off = XF == E4M3 ? 32 * b + 16 * (rg & 1) : 16 * b;
-                    const int4v v = *reinterpret_cast<const int4v *>(row + (b < KB ? off : 0));
-                    xf[f][j].c[c] = b < KB ? v : int4v{0, 0, 0, 0};
-                }
+                for (int j = 0; j < SPW; ++j)
+#pragma unroll
+                    for (int c = 0; c < XH; ++c) {
+                        const int b = XF == E4M3 ? bw + SPW * (2 * c + (rg >> 1)) + j : bw + SPW * rg + j;
+                        const int off = XF == E4M3 ? 32 * b + 16 * (rg & 1) : 16 * b;
+                        const int4v q = *reinterpret_cast<const int4v *>(row + (b < KB ? off : 0));
+                        xf[f][v][j].c[c] = b < KB ? q : int4v{0, 0, 0, 0};
+                    }
+            }
         }
 #pragma unroll
         for (int i = 0; i < NG; ++i) {
-            const int n = n0 + i * 16 + ri < N ? n0 + i * 16 + ri : N - 1;
-            dec_scales<SPW>(p.ws + (int64_t)n * KB, b0 + SPW * rg, KB, sw[i]);
+            const int n = i * 16 + ri < ntop ? i * 16 + ri : ntop;
+            const uint8_t *row = p.ws + (int64_t)(n0 + n) * KB;
+#pragma unroll
+            for (int v = 0; v < WPW; ++v)
+                sw[i][v] = dec_scales<SPW>(row, ((pass * WPW + v) * NW + wave) * WB + SPW * rg, KB);
         }
 #pragma unroll
         for (int i = 0; i < NG; ++i) {
             if (i < ng) {
-                // Stage t has landed once at most min(S - 2, nst - 1 - t)
-                // later ones are in flight (loads complete in order).
-                wait_stages<S - 2, SPW>(nst - 1 - t);
-                asm volatile("" ::: "memory");  // no read of the stage moves above the wait
-                if (t + S - 1 < nst) {
-                    // slot (t - 1) % S is refilled: its reads must be done
-                    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-                    issue(t + S - 1);
-                }
-                const uint8_t *sb = rd + (t % S) * SLOT;
-                int4v wf[SPW];
 #pragma unroll
-                for (int j = 0; j < SPW; ++j)
-                    wf[j] = *reinterpret_cast<const int4v *>(sb + (((SPW * rg + j) ^ fsw) << 4));
-                auto step = [&](auto jc) {
-                    constexpr int J = decltype(jc)::value;
-                    if constexpr (J < SPW) {
-#pragma unroll
-                        for (int f = 0; f < FT; ++f)
-                            acc[i][f] = mfma16<XF, (J & 3)>(wf[J], xf[f][J], acc[i][f],
-                                                            (int)sw[i][J / 4], (int)sx[f][J / 4]);
+                for (int v = 0; v < WPW; ++v) {
+                    // Stage t has landed once at most min(S - 2, nst - 1 - t)
+                    // later ones are in flight (loads complete in order).
+                    wait_stages<S - 2, SPW>(nst - 1 - t);
+                    asm volatile("" ::: "memory");  // no read of the stage moves above the wait
+                    if (t + S - 1 < nst) {
+                        // the slot of stage t - 1 is refilled: its reads must be done
+                        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                        issue();
                     }
-                };
-                step(std::integral_constant<int, 0>{});
-                step(std::integral_constant<int, 1>{});
-                step(std::integral_constant<int, 2>{});
-                step(std::integral_constant<int, 3>{});
-                step(std::integral_constant<int, 4>{});
-                step(std::integral_constant<int, 5>{});
-                step(std::integral_constant<int, 6>{});
-                step(std::integral_constant<int, 7>{});
-                ++t;
+                    const uint8_t *sb = rd + slot * SLOT;
+                    int4v wf[SPW];
+#pragma unroll
+                    for (int j = 0; j < SPW; ++j)
+                        wf[j] = *reinterpret_cast<const int4v *>(sb + (((SPW * rg + j) ^ fsw) << 4));
+                    auto step = [&](auto jc) {
+                        constexpr int J = decltype(jc)::value;
+                        if constexpr (J < SPW) {
+#pragma unroll
+                            for (int f = 0; f < FT; ++f)
+                                acc[i][f] = mfma16<XF, J>(wf[J], xf[f][v][J], acc[i][f],
+                                                          (int)sw[i][v], (int)sx[f][v]);
+                        }
+                    };
+                    step(std::integral_constant<int, 0>{});
+                    step(std::integral_constant<int, 1>{});
+                    step(std::integral_constant<int, 2>{});
+                    step(std::integral_constant<int, 3>{});
+                    ++t;
+                    slot = slot + 1 == S ? 0 : slot + 1;
+                }
             }
         }
     }
@@ -649,57 +637,60 @@ __global__ __launch_bounds__(512, 1) void mx_gemm_dec(MxArgs p) {
     __syncthreads();  // every wave is done with its ring: reuse it for the sums
 
     // 16x16 accumulator layout: lane l, register v holds weight row
-    // 4 (l / 16) + v and token l % 16.  red[wave][group][f][token][row].
-    float *red = reinterpret_cast<float *>(smem);
+    // 4 (l / 16) + v and token l % 16.
+    f32x4 *red = reinterpret_cast<f32x4 *>(smem);  // [wave][group][f][slot]
 #pragma unroll
     for (int i = 0; i < NG; ++i)
         if (i < ng) {
 #pragma unroll
             for (int f = 0; f < FT; ++f)
-                *reinterpret_cast<f32x4 *>(red + ((wave * NG + i) * FT + f) * 256 + ri * 16 + 4 * rg) =
-                    acc[i][f];
+                red[((wave * NG + i) * FT + f) * 64 + join_slot(ri, rg, i)] = acc[i][f];
         }
     __syncthreads();
-    const int cols = ng * 16;
-    for (int e = tid; e < cols * M; e += 512) {
-        const int nl = e % cols, m = e / cols;
-        if (n0 + nl >= N) continue;
-        const float *r = red + ((nl >> 4) * FT + (m >> 4)) * 256 + (m & 15) * 16 + (nl & 15);
-        float s = 0.0f;
+    using T = typename OutT<YDT>::T;
+    const int quads = ng * 4;  // four successive outputs a thread
+    const bool vec_y = ((int64_t)N * (int)sizeof(T)) % (4 * (int)sizeof(T)) == 0 &&
+                       ((uintptr_t)p.y % (4 * sizeof(T))) == 0;
+    for (int e = tid; e < quads * M; e += 512) {
+        const int nq = e % quads, m = e / quads;
+        const int g = nq >> 2, n = n0 + nq * 4;
+        if (n >= N) continue;
+        const f32x4 *r = red + (g * FT + (m >> 4)) * 64 + join_slot(m & 15, nq & 3, g);
+        f32x4 s = r[0];
 #pragma unroll
-        for (int w = 0; w < NW; ++w) s += r[w * (NG * FT * 256)];
-        mx_store_y<YDT>(p.y, (int64_t)m * N + n0 + nl, s);
+        for (int w = 1; w < NW; ++w) s += r[w * (NG * FT * 64)];
+        T h[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) h[k] = narrow<YDT>(s[k]);
+        T *yp = reinterpret_cast<T *>(p.y) + (ms + m) * N + n;
+        if (vec_y) {  // N % 4 == 0: all four or none
+            if constexpr (sizeof(T) == 4) *reinterpret_cast<uint4 *>(yp) = __builtin_bit_cast(uint4, h);
+            else *reinterpret_cast<uint2 *>(yp) = __builtin_bit_cast(uint2, h);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (n + k < N) yp[k] = h[k];
+        }
     }
 }
 
 // ---------------------------------------------------------------- launch
 
-template <int XF, int BM, int BN, int WM, int WN, int STA>
-static void launch_pp(MxArgs &a, int y_dt, hipStream_t stream) {
+template <int XF, int BM, int BN, int WM, int WN, int STA, int CH>
+static void launch_pp(MxArgs &a, hipStream_t stream) {
     const int tm = (a.M + BM - 1) / BM, tn = (a.N + BN - 1) / BN;
     set_xcd_grid(a, tm, tn, BM, BN);
     const dim3 grid((unsigned)(tm * tn)), block(64 * WM * WN);
-    if (y_dt == F32) mx_gemm_pp<XF, BM, BN, WM, WN, STA, F32><<<grid, block, 0, stream>>>(a);
-    else if (y_dt == F16) mx_gemm_pp<XF, BM, BN, WM, WN, STA, F16><<<grid, block, 0, stream>>>(a);
-    else mx_gemm_pp<XF, BM, BN, WM, WN, STA, BF16><<<grid, block, 0, stream>>>(a);
+    mx_gemm_pp<XF, BM, BN, WM, WN, STA, CH><<<grid, block, 0, stream>>>(a);
 }
 
-template <int XF>
-static void launch_tile(MxArgs &a, int y_dt, hipStream_t stream) {
-    const int tm = (a.M + 127) / 128, tn = (a.N + 127) / 128;
-    set_xcd_grid(a, tm, tn, 128, 128);
-    const dim3 grid((unsigned)(tm * tn));
-    if (y_dt == F32) mx_gemm_tile<XF, F32><<<grid, 256, 0, stream>>>(a);
-    else if (y_dt == F16) mx_gemm_tile<XF, F16><<<grid, 256, 0, stream>>>(a);
-    else mx_gemm_tile<XF, BF16><<<grid, 256, 0, stream>>>(a);
-}
-
-template <int XF, int FT, int SPW, int NG, int S>
+template <int XF, int FT, int SPW, int WPW, int NG, int S>
 static void launch_dec_t(MxArgs &a, int y_dt, hipStream_t stream) {
-    const dim3 grid((unsigned)((a.N + 16 * a.groups - 1) / (16 * a.groups)));
-    if (y_dt == F32) mx_gemm_dec<XF, FT, SPW, NG, S, F32><<<grid, 512, 0, stream>>>(a);
-    else if (y_dt == F16) mx_gemm_dec<XF, FT, SPW, NG, S, F16><<<grid, 512, 0, stream>>>(a);
-    else mx_gemm_dec<XF, FT, SPW, NG, S, BF16><<<grid, 512, 0, stream>>>(a);
+    const dim3 grid((unsigned)((a.N + 16 * a.groups - 1) / (16 * a.groups)),
+                    (unsigned)((a.M + 16 * FT - 1) / (16 * FT)));
+    if (y_dt == F32) mx_gemm_dec<XF, FT, SPW, WPW, NG, S, F32><<<grid, 512, 0, stream>>>(a);
+    else if (y_dt == F16) mx_gemm_dec<XF, FT, SPW, WPW, NG, S, F16><<<grid, 512, 0, stream>>>(a);
+    else mx_gemm_dec<XF, FT, SPW, WPW, NG, S, BF16><<<grid, 512, 0, stream>>>(a);
 }
 
 template <int XF, int FT>
@@ -709,40 +700,37 @@ static void launch_dec(MxArgs &a, int y_dt, hipStream_t stream) {
     const int64_t groups = ((int64_t)a.N + 15) / 16;
     const int64_t rounds = (groups + 256 * 8 - 1) / (256 * 8);
     a.groups = (int)((groups + 256 * rounds - 1) / (256 * rounds));
-    // the window that lets eight waves cover K, at most 1024 elements (512
-    // where the activations of 32 rows would not fit the registers)
-    constexpr bool kWide = XF == E2M1 || FT == 1;
-    const int spw = a.K <= 1024 ? 1 : a.K <= 2048 ? 2 : a.K <= 4096 || !kWide ? 4 : 8;
+    // the windows that let eight waves cover K, at most 1024 elements a wave
+    // (512 where the activations of 32 rows would not fit the registers)
+    constexpr int kMaxWpw = XF == E2M1 || FT == 1 ? 2 : 1;
     const bool many = a.groups > 2;
-    if (spw == 8) {
-        if constexpr (kWide) {
-            if (many) launch_dec_t<XF, FT, 8, 8, 2>(a, y_dt, stream);
-            else launch_dec_t<XF, FT, 8, 2, 2>(a, y_dt, stream);
-        }
-    } else if (spw == 4) {
-        if (many) launch_dec_t<XF, FT, 4, 8, 4>(a, y_dt, stream);
-        else launch_dec_t<XF, FT, 4, 2, 3>(a, y_dt, stream);
-    } else if (spw == 2) {
-        if (many) launch_dec_t<XF, FT, 2, 8, 6>(a, y_dt, stream);
-        else launch_dec_t<XF, FT, 2, 2, 3>(a, y_dt, stream);
-    } else {
-        if (many) launch_dec_t<XF, FT, 1, 8, 8>(a, y_dt, stream);
-        else launch_dec_t<XF, FT, 1, 2, 3>(a, y_dt, stream);
+    if (a.K <= 1024) {
+        if (many) launch_dec_t<XF, FT, 1, 1, 8, 8>(a, y_dt, stream);
+        else launch_dec_t<XF, FT, 1, 1, 2, 3>(a, y_dt, stream);
+    } else if (a.K <= 2048) {
+        if (many) launch_dec_t<XF, FT, 2, 1, 8, 6>(a, y_dt, stream);
+        else launch_dec_t<XF, FT, 2, 1, 2, 3>(a, y_dt, stream);
+    } else if (a.K <= 4096 || kMaxWpw == 1) {
+        if (many) launch_dec_t<XF, FT, 4, 1, 8, 4>(a, y_dt, stream);
+        else launch_dec_t<XF, FT, 4, 1, 2, 3>(a, y_dt, stream);
+    } else if constexpr (kMaxWpw == 2) {
+        if (many) launch_dec_t<XF, FT, 4, 2, 8, 4>(a, y_dt, stream);
+        else launch_dec_t<XF, FT, 4, 2, 2, 4>(a, y_dt, stream);
     }
 }
 
 template <int XF>
 static void launch_mx(MxArgs &a, int y_dt, hipStream_t stream, int tile) {
     if (a.M <= 16) return launch_dec<XF, 1>(a, y_dt, stream);
-    if (a.M <= 32) return launch_dec<XF, 2>(a, y_dt, stream);
-    if (a.K % 128 != 0 || a.K < 256) return launch_tile<XF>(a, y_dt, stream);
+    if (a.M <= 32 || a.K < 256) return launch_dec<XF, 2>(a, y_dt, stream);
+    if (a.K % 128 != 0) return launch_pp<XF, 128, 128, 2, 2, 2, 0>(a, stream);
     if constexpr (XF == E2M1) {
-        if (tile == 0) launch_pp<XF, 256, 256, 4, 2, 2>(a, y_dt, stream);
-        else if (tile == 1) launch_pp<XF, 256, 128, 4, 2, 3>(a, y_dt, stream);
-        else launch_pp<XF, 128, 128, 2, 2, 2>(a, y_dt, stream);
+        if (tile == 0) launch_pp<XF, 256, 256, 4, 2, 2, 2>(a, stream);
+        else if (tile == 1) launch_pp<XF, 256, 128, 4, 2, 3, 4>(a, stream);
+        else launch_pp<XF, 128, 128, 2, 2, 2, 4>(a, stream);
     } else {
-        if (tile == 0) launch_pp<XF, 128, 256, 2, 4, 2>(a, y_dt, stream);
-        else launch_pp<XF, 128, 128, 2, 2, 2>(a, y_dt, stream);
+        if (tile == 0) launch_pp<XF, 128, 256, 2, 4, 2, 4>(a, stream);
+        else launch_pp<XF, 128, 128, 2, 2, 2, 4>(a, stream);
     }
 }
 
@@ -768,7 +756,7 @@ void launch_gemm_mx(const uint8_t *xq, const uint8_t *xs, int x_fmt, const uint8
                     hipStream_t stream, int force_tile) {
     MxArgs a{};
     a.xq = xq; a.xs = xs; a.wq = wq; a.ws = ws;
-    a.M = (int)M; a.N = (int)N; a.K = (int)K; a.y = y;
+    a.M = (int)M; a.N = (int)N; a.K = (int)K; a.y = y; a.y_dt = y_dt;
     const int tile = force_tile >= 0 ? force_tile : mx_pick_tile(x_fmt, M, N);
     if (x_fmt == E2M1) launch_mx<E2M1>(a, y_dt, stream, tile);
     else launch_mx<E4M3>(a, y_dt, stream, tile);
