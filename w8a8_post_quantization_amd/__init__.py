@@ -112,14 +112,16 @@ def lib():
 
 
 _torch_mod = None
+_raw_stream = None  # torch's current-stream handle by device, where it has one
 _dt_codes = {}
 
 
 def _torch():
-    global _torch_mod
+    global _torch_mod, _raw_stream
     if _torch_mod is None:
         import torch
 
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         _dt_codes.update({torch.float32: SQ_F32, torch.float16: SQ_F16, torch.bfloat16: SQ_BF16})
         _torch_mod = torch
     return _torch_mod
@@ -156,10 +158,9 @@ def _stream(stream=None):
     if stream is not None:
         return ctypes.c_void_p(stream.cuda_stream)
     # the current stream's handle alone costs 0.3 us, the Stream object 2.7 us
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    if raw is None:
+    if _raw_stream is None:
         return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
-    return ctypes.c_void_p(raw(torch.cuda.current_device()))
+    return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()))
 
 
 def _call(name, *args):
@@ -469,20 +470,37 @@ def gemm_fp8_dequant(xq, wq, x_scale, w_scale, out_dtype=None, out=None, stream=
 
 # ------------------------------------------------------- microscaled (MX)
 
+_mx_fns = {}
+
+
 def _mx_call(name, tensors, args, stream, *last):
     """Call `name` on the operands' own GPU.  `tensors` are all the operands
     (None allowed, the first present); `stream` (or that GPU's current stream)
     gets the work; `last` are the arguments behind the stream."""
+    fn = _mx_fns.get(name)
+    if fn is None:
+        fn = _mx_fns[name] = getattr(lib(), name)
     dev = tensors[0].get_device()
     for t in tensors:
         if t is not None and t.get_device() != dev:
             raise ValueError(f"operands on {tensors[0].device} and {t.device}")
-    cuda = _torch().cuda
+    cuda = _torch_mod.cuda
     if cuda.current_device() == dev:
-        _call(name, *args, _stream(stream), *last)
+        if stream is None and _raw_stream is not None:
+            status = fn(*args, _raw_stream(dev), *last)
+        else:
+            status = fn(*args, _stream(stream), *last)
     else:
         with cuda.device(dev):
-            _call(name, *args, _stream(stream), *last)
+            status = fn(*args, _stream(stream), *last)
+    if status != 0:
+        raise SQError(name, status)
+
+
+def _mx_check(t, name, dtypes, ndim):
+    """_check's conditions in one expression (these calls are latency-bound)."""
+    if not (t.is_cuda and t.dtype in dtypes and t.dim() == ndim and t.is_contiguous()):
+        _check(t, name, dtypes, ndim)
 
 
 def _mx_codes(fmt, K):
@@ -495,8 +513,8 @@ def _mx_codes(fmt, K):
 def _mx_shapes(q, scale, fmt, name):
     """(rows, K) of codes [rows, K / 2] or [rows, K] and scales [rows, K / 32]."""
     u8 = (_torch().uint8,)
-    _check(q, name, u8, 2)
-    _check(scale, "the scales of " + name, u8, 2)
+    _mx_check(q, name, u8, 2)
+    _mx_check(scale, "the scales of codes", u8, 2)
     (rows, codes), (srows, blocks) = q.shape, scale.shape
     if codes != _mx_codes(fmt, blocks * 32) or srows != rows:
         raise ValueError(f"{name} {tuple(q.shape)} and its scales {tuple(scale.shape)} disagree")
@@ -507,9 +525,9 @@ def _mx_out(out, rows, K, fmt, device):
     if K % 32:
         raise ValueError(f"rows of {K} elements: a multiple of 32 is needed")
     if out is None:
-        torch = _torch()
-        return (torch.empty((rows, _mx_codes(fmt, K)), dtype=torch.uint8, device=device),
-                torch.empty((rows, K // 32), dtype=torch.uint8, device=device))
+        empty, u8 = _torch_mod.empty, _torch_mod.uint8
+        return (empty((rows, _mx_codes(fmt, K)), dtype=u8, device=device),
+                empty((rows, K // 32), dtype=u8, device=device))
     q, scale = out
     if _mx_shapes(q, scale, fmt, "out") != (rows, K):
         raise ValueError(f"out {tuple(q.shape)} does not fit {rows} rows of {K} elements")
@@ -520,16 +538,16 @@ def _vector(t, name, n):
     """The pointer of an fp32 vector of n elements, or None."""
     if t is None:
         return None
-    _check(t, name, (_torch().float32,), 1)
-    if t.numel() != n:
-        raise ValueError(f"{name} has {t.numel()} elements, not {n}")
+    _mx_check(t, name, (_torch_mod.float32,), 1)
+    if t.shape[0] != n:
+        raise ValueError(f"{name} has {t.shape[0]} elements, not {n}")
     return t.data_ptr()
 
 
 def _mx_rows(x, name):
-    torch = _torch()
+    _torch()
     x2 = x if x.dim() == 2 else x.reshape(-1, x.shape[-1])
-    _check(x2, name, (torch.float32, torch.float16, torch.bfloat16))
+    _mx_check(x2, name, _dt_codes, 2)
     return x2
 
 
@@ -541,20 +559,20 @@ def quantize_act_mx(x, inv_s=None, fmt=SQ_MX_E2M1, out=None, stream=None):
     inv = _vector(inv_s, "inv_s", K)
     xq, xs = _mx_out(out, M, K, fmt, x2.device)
     _mx_call("sq_quantize_act_mx", (x2, inv_s, xq, xs),
-             (x2.data_ptr(), _dt(x2), M, K, inv, fmt, xq.data_ptr(), xs.data_ptr()), stream)
+             (x2.data_ptr(), _dt_codes[x2.dtype], M, K, inv, fmt, xq.data_ptr(), xs.data_ptr()), stream)
     return xq, xs
 
 
 def smooth_weights_mxfp4(w, s=None, row_mul=None, out=None, stream=None):
     """a3 in MX: (wq uint8 [N, K/2] e2m1, w_scale uint8 [N, K/32]) of
     fl(fl(w * row_mul[n]) * s[k]); row_mul and s as in smooth_weights."""
-    torch = _torch()
-    _check(w, "w", (torch.float32, torch.float16, torch.bfloat16), 2)
+    _torch()
+    _mx_check(w, "w", _dt_codes, 2)
     N, K = w.shape
     sp, rp = _vector(s, "s", K), _vector(row_mul, "row_mul", N)
     wq, ws = _mx_out(out, N, K, SQ_MX_E2M1, w.device)
     _mx_call("sq_smooth_weights_mxfp4", (w, s, row_mul, wq, ws),
-             (w.data_ptr(), _dt(w), N, K, rp, sp, wq.data_ptr(), ws.data_ptr()), stream)
+             (w.data_ptr(), _dt_codes[w.dtype], N, K, rp, sp, wq.data_ptr(), ws.data_ptr()), stream)
     return wq, ws
 
 
@@ -568,7 +586,7 @@ def norm_quantize_act_mx(x, gamma, beta=None, norm=SQ_NORM_LAYER, eps=1e-5, fmt=
     g, b = _vector(gamma, "gamma", K), _vector(beta, "beta", K)
     xq, xs = _mx_out(out, M, K, fmt, x2.device)
     _mx_call("sq_norm_quantize_act_mx", (x2, gamma, beta, xq, xs),
-             (x2.data_ptr(), _dt(x2), M, K, norm, g, b, eps, fmt, xq.data_ptr(), xs.data_ptr()),
+             (x2.data_ptr(), _dt_codes[x2.dtype], M, K, norm, g, b, eps, fmt, xq.data_ptr(), xs.data_ptr()),
              stream)
     return xq, xs
 
@@ -580,11 +598,11 @@ def dequantize_mx(q, scale, fmt=SQ_MX_E2M1, out_dtype=None, out=None, stream=Non
     rows, K = _mx_shapes(q, scale, fmt, "q")
     y = out if out is not None else torch.empty((rows, K), dtype=out_dtype or torch.float32,
                                                 device=q.device)
-    _check(y, "out", (torch.float32, torch.float16, torch.bfloat16), 2)
+    _mx_check(y, "out", _dt_codes, 2)
     if tuple(y.shape) != (rows, K):
         raise ValueError(f"out {tuple(y.shape)} is not {(rows, K)}")
     _mx_call("sq_dequantize_mx", (q, scale, y),
-             (q.data_ptr(), scale.data_ptr(), fmt, rows, K, y.data_ptr(), _dt(y)), stream)
+             (q.data_ptr(), scale.data_ptr(), fmt, rows, K, y.data_ptr(), _dt_codes[y.dtype]), stream)
     return y
 
 
@@ -600,11 +618,11 @@ def gemm_mxfp4(xq, x_scale, wq, w_scale, x_fmt=SQ_MX_E2M1, out_dtype=None, out=N
         raise ValueError(f"K mismatch: xq has {K}, wq {Kw}")
     y = out if out is not None else torch.empty((M, N), dtype=out_dtype or torch.float16,
                                                 device=xq.device)
-    _check(y, "out", (torch.float32, torch.float16, torch.bfloat16), 2)
+    _mx_check(y, "out", _dt_codes, 2)
     if tuple(y.shape) != (M, N):
         raise ValueError(f"out {tuple(y.shape)} is not {(M, N)}")
     args = (xq.data_ptr(), x_scale.data_ptr(), x_fmt, wq.data_ptr(), w_scale.data_ptr(), M, N, K,
-            y.data_ptr(), _dt(y))
+            y.data_ptr(), _dt_codes[y.dtype])
     if tile is None:
         _mx_call("sq_gemm_mxfp4", (xq, x_scale, wq, w_scale, y), args, stream)
     else:

@@ -550,10 +550,42 @@ __global__ __launch_bounds__(512, 1) void mx_gemm_dec(MxArgs p) {
             }
         }
     };
-    const int nst = passes * ng * WPW;
+    // Activations.  Up to 16 rows: each lane loads its own chunks (few lines
+    // an instruction where rows repeat or are few).  More rows (XRING): such
+    // loads would look up 64 lines each (27.3 us against 26.0 at M = 32, N = 28672,
+    // K = 8192),
+    // so the rows come through the ring, XST stages before a pass's weights:
+    // 16 rows of a window's 64 SPW bytes, or of one of its halves (e4m3).
+    constexpr bool XRING = FT > 1;
+    constexpr int XST = XRING ? FT * WPW * XH : 0;
+    int ix = 0;  // activation stages of the pass issued
+    auto issue_x = [&]() {
+        const int f = ix / (WPW * XH), v = ix / XH % WPW, hh = ix % XH;
+        const int c0 = ((ip * WPW + v) * NW + wave) * (WB * XH) + hh * CPR;  // the stage's first chunk
+        uint32_t off[SPW];
+#pragma unroll
+        for (int i = 0; i < SPW; ++i) {
+            const int r = i * RPI + lrow;
+            const int m = f * 16 + r < M ? f * 16 + r : M - 1;
+            const int c = c0 + (lpos ^ dec_chunk_swz<SPW>(r));
+            off[i] = ((uint32_t)m * (uint32_t)(KB * XH) + (c < KB * XH ? c : 0)) * 16u + dma_bias<16>(i);
+        }
+        lds_dma_based<SPW, 16, false>(off, xq, ring + (uint32_t)(islot * SLOT));
+        islot = islot + 1 == S ? 0 : islot + 1;
+        ++ix;
+    };
+    auto issue_next = [&]() {
+        if (XRING && ix < XST) {
+            issue_x();
+        } else {
+            issue();
+            if (XRING && iw == 0 && ig == 0) ix = 0;  // the next pass
+        }
+    };
+    const int nst = passes * (ng * WPW + XST);
 #pragma unroll
     for (int t = 0; t < S - 1; ++t)
-        if (t < nst) issue();
+        if (t < nst) issue_next();
 
     f32x4 acc[NG][FT];
 #pragma unroll
@@ -564,6 +596,23 @@ __global__ __launch_bounds__(512, 1) void mx_gemm_dec(MxArgs p) {
     const int fsw = dec_chunk_swz<SPW>(ri);
 
     int t = 0, slot = 0;
+    // Wait for stage t, refill the ring, and the address of the stage's row of
+    // this lane.
+    auto next_stage = [&]() {
+        // Stage t has landed once at most min(S - 2, nst - 1 - t) later ones
+        // are in flight (loads complete in order).
+        wait_stages<S - 2, SPW>(nst - 1 - t);
+        asm volatile("" ::: "memory");  // no read of the stage moves above the wait
+        if (t + S - 1 < nst) {
+            // the slot of stage t - 1 is refilled: its reads must be done
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            issue_next();
+        }
+        const uint8_t *sb = rd + slot * SLOT;
+        ++t;
+        slot = slot + 1 == S ? 0 : slot + 1;
+        return sb;
+    };
     for (int pass = 0; pass < passes; ++pass) {
         // this pass's activations and every group's weight scales
         XFrag<XF> xf[FT][WPW][SPW];
@@ -576,6 +625,7 @@ __global__ __launch_bounds__(512, 1) void mx_gemm_dec(MxArgs p) {
             for (int v = 0; v < WPW; ++v) {
                 const int bw = ((pass * WPW + v) * NW + wave) * WB;
                 sx[f][v] = dec_scales<SPW>(xs + (int64_t)m * KB, bw + SPW * rg, KB);
+                if constexpr (XRING) continue;
 #pragma unroll
                 for (int j = 0; j < SPW; ++j)
 #pragma unroll
@@ -595,21 +645,39 @@ __global__ __launch_bounds__(512, 1) void mx_gemm_dec(MxArgs p) {
             for (int v = 0; v < WPW; ++v)
                 sw[i][v] = dec_scales<SPW>(row, ((pass * WPW + v) * NW + wave) * WB + SPW * rg, KB);
         }
+        if constexpr (XRING) {
+            // (the scale words are taken before the first stage: a wait for
+            // them later would wait for the whole ring)
+#pragma unroll
+            for (int v = 0; v < WPW; ++v) {
+#pragma unroll
+                for (int f = 0; f < FT; ++f) asm volatile("" : "+v"(sx[f][v]));
+#pragma unroll
+                for (int i = 0; i < NG; ++i) asm volatile("" : "+v"(sw[i][v]));
+            }
+#pragma unroll
+            for (int f = 0; f < FT; ++f)
+#pragma unroll
+                for (int v = 0; v < WPW; ++v)
+#pragma unroll
+                    for (int c = 0; c < XH; ++c) {
+                        const uint8_t *sb = next_stage();
+                        const int bw = ((pass * WPW + v) * NW + wave) * WB;
+#pragma unroll
+                        for (int j = 0; j < SPW; ++j) {
+                            const int b = XF == E4M3 ? bw + SPW * (2 * c + (rg >> 1)) + j : bw + SPW * rg + j;
+                            const int ch = XF == E4M3 ? 2 * (SPW * (rg >> 1) + j) + (rg & 1) : SPW * rg + j;
+                            const int4v q = *reinterpret_cast<const int4v *>(sb + ((ch ^ fsw) << 4));
+                            xf[f][v][j].c[c] = b < KB ? q : int4v{0, 0, 0, 0};
+                        }
+                    }
+        }
 #pragma unroll
         for (int i = 0; i < NG; ++i) {
             if (i < ng) {
 #pragma unroll
                 for (int v = 0; v < WPW; ++v) {
-                    // Stage t has landed once at most min(S - 2, nst - 1 - t)
-                    // later ones are in flight (loads complete in order).
-                    wait_stages<S - 2, SPW>(nst - 1 - t);
-                    asm volatile("" ::: "memory");  // no read of the stage moves above the wait
-                    if (t + S - 1 < nst) {
-                        // the slot of stage t - 1 is refilled: its reads must be done
-                        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-                        issue();
-                    }
-                    const uint8_t *sb = rd + slot * SLOT;
+                    const uint8_t *sb = next_stage();
                     int4v wf[SPW];
 #pragma unroll
                     for (int j = 0; j < SPW; ++j)
@@ -627,8 +695,6 @@ __global__ __launch_bounds__(512, 1) void mx_gemm_dec(MxArgs p) {
                     step(std::integral_constant<int, 1>{});
                     step(std::integral_constant<int, 2>{});
                     step(std::integral_constant<int, 3>{});
-                    ++t;
-                    slot = slot + 1 == S ? 0 : slot + 1;
                 }
             }
         }
