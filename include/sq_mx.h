@@ -71,9 +71,8 @@ int sq_smooth_weights_mxfp4(const void *w, int dt, int64_t N, int64_t K, const f
  *   x      [M, K] of dt (SQ_F32, SQ_F16 or SQ_BF16)
  *   norm   SQ_NORM_LAYER: mu = mean_j x_j, sigma^2 = mean_j (x_j - mu)^2;
  *          SQ_NORM_RMS:   mu = 0,          sigma^2 = mean_j x_j^2
- *          summed in double (the result of a row does not depend on M or on
- *          the other rows); rstd = 1 / sqrt(sigma^2 + eps) in double; then
- *          mu and rstd rounded to fp32
+ *          summed in double; rstd = 1 / sqrt(sigma^2 + eps) in double; then mu
+ *          and rstd rounded to fp32
  *   gamma  [K] fp32; beta [K] fp32 or NULL; eps >= 0, finite
  *   per element in fp32: n = fl(fl(x - mu) * rstd), y = fl(n * gamma_j), then
  *          y = fl(y + beta_j) if beta

@@ -211,7 +211,8 @@ def test_dequantize_every_code_and_scale(torch, fmt):
     (65, 2080, "f16", True, True), (257, 1024, "bf16", True, False), (5, 16384, "f16", True, True),
     (7, 16384, "f32", False, True), (1030, 4096, "f16", False, False), (2050, 7168, "f16", True, True),
     (1500, 1056, "f32", True, True), (1100, 2048, "bf16", False, True), (4100, 512, "f16", True, False),
-    (1025, 10240, "bf16", True, True)])
+    (1025, 10240, "bf16", True, True), (4097, 4128, "f16", True, True), (4100, 8192, "bf16", False, True),
+    (4096, 7168, "f16", True, False)])
 def test_norm_parity(torch, M, K, dt, layer, beta, fmt):
     a = synth.normal(M + K, 1, (M, K)).astype(np.float32) * np.float32(2) + np.float32(0.25)
     a[:, synth.choose(M + K, 2, K, 2)] *= np.float32(60)

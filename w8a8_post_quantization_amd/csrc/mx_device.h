@@ -54,13 +54,12 @@ template <int FMT> struct MxCodes { uint32_t w[FMT == E2M1 ? 1 : 2]; };
 
 template <int FMT>
 __device__ __forceinline__ MxCodes<FMT> mx_encode8(const float (&v)[8], uint32_t &e_out) {
-    uint32_t b = 0;
+    // the largest |v| of the lane, a NaN if there is one (IEEE maximum: three
+    // operands and their magnitudes an instruction)
+    float top = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t u = __float_as_uint(v[i]) & 0x7fffffffu;
-        b = b > u ? b : u;
-    }
-    b = quad_max(b);
+    for (int i = 0; i < 8; ++i) top = __builtin_elementwise_maximum(top, __builtin_fabsf(v[i]));
+    const uint32_t b = quad_max(__float_as_uint(top) & 0x7fffffffu);
     constexpr int P = FMT == E2M1 ? 2 : 8;
     const int E = (int)(b >> 23);
     const int e = E > P ? E - P : 0;
@@ -80,12 +79,12 @@ __device__ __forceinline__ MxCodes<FMT> mx_encode8(const float (&v)[8], uint32_t
     } else {
         // the e4m3 conversion turns magnitudes above 464 into NaN: clamp to
         // 448 s = 1.75 2^(e - 119) first
-        const float top = __uint_as_float(((uint32_t)(e + 8) << 23) | 0x00600000u);
+        const float lim = __uint_as_float(((uint32_t)(e + 8) << 23) | 0x00600000u);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             float z[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) z[i] = __builtin_amdgcn_fmed3f(v[4 * h + i], -top, top);
+            for (int i = 0; i < 4; ++i) z[i] = __builtin_amdgcn_fmed3f(v[4 * h + i], -lim, lim);
             short2v w = {0, 0};
             w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, z[0], z[1], s, false);
             w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, z[2], z[3], s, true);

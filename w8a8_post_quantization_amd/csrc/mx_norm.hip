@@ -2,109 +2,327 @@
 // SmoothQuant tutorial page, section 融入 LayerNorm, as the int8 form in
 // norm.hip, with a block scale for every 32 outputs instead of a row step.
 //
-// Statistics in double from one pass over the registers, with a pivot p (the
-// row's first element): S1 = sum (x - p), S2 = sum (x - p)^2,
-//   mu = p + S1 / K, sigma^2 = S2 / K - (S1 / K)^2
-// (RMS: p = 0, sigma^2 = S2 / K).  The subtraction loses little: one element
-// of K gives (p - mu)^2 <= K sigma^2, so S2 / K <= (K + 1) sigma^2 and the
-// relative error of sigma^2 stays near K 2^-52 <= 2^-38, against the fp32
-// rounding of rstd that follows.
+// Statistics in double: S1 = sum x, S2 = sum x^2 in one pass over the
+// registers, mu = S1 / K, sigma^2 = S2 / K - mu^2.  The subtraction keeps
+// sigma^2 to a relative 2^-53 (K / (64 NW) + 8) mu^2 / sigma^2, so where
+// mu^2 > 2^8 sigma^2 a second pass forms sum (x - mu)^2 instead: either way
+// the error is below 2^-39, against the fp32 rounding of rstd that follows.
+// (The fp64 conversions and sums weigh most in the kernel's issue time; a
+// pivot subtracted from every element would need no second pass, but one more
+// of them for each element.)
+#include <type_traits>
+
 #include "mx_device.h"
 #include "sq_launch.h"
 
 namespace sq {
 
-__device__ __forceinline__ double wave_sum(double v) {
+// 1 / sqrt(v) for v > 0: the hardware estimate and two Newton steps, within a
+// few units of a double's last place (1.0 / sqrt(v) rounds correctly twice,
+// in six times the instructions; the result is rounded to fp32 here).
+__device__ __forceinline__ double inv_sqrt(double v) {
+    double y = __builtin_amdgcn_rsq(v);
+    const double h = 0.5 * v;
 #pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, kWave);
-    return v;
+    for (int i = 0; i < 2; ++i) {
+        const double e = __builtin_fma(-h * y, y, 0.5);  // (1 - v y^2) / 2
+        y = __builtin_fma(y, e, y);
+    }
+    return y;
 }
 
-template <int DT>
-__device__ __forceinline__ float first_of(const void *x, int64_t i) {
-    if constexpr (DT == F32) return reinterpret_cast<const float *>(x)[i];
-    else if constexpr (DT == F16) return (float)reinterpret_cast<const _Float16 *>(x)[i];
-    else return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t *>(x)[i] << 16);
+// (0 for a zero row with eps = 0: 1 / sqrt(0), an infinity as defined)
+__device__ __forceinline__ float row_rstd(double ve) {
+    return ve > 0.0 ? (float)inv_sqrt(ve) : (float)(1.0 / sqrt(ve));
 }
 
-// A block per row; thread t holds column groups t + 256 i, i < ITS.
-template <int DT, int FMT, int NORM, bool HAS_BETA, int ITS>
-__global__ __launch_bounds__(256) void mx_norm_kernel(const void *__restrict__ x, int64_t K,
-                                                      const float *__restrict__ gamma,
-                                                      const float *__restrict__ beta, float eps,
-                                                      uint8_t *__restrict__ q,
-                                                      uint8_t *__restrict__ scale) {
-    __shared__ double red[2][4];
-    const int64_t row = blockIdx.x;
+// The wave's value of lane 63, in every lane.
+__device__ __forceinline__ double of_lane63(double v) {
+    const uint64_t u = (uint64_t)__double_as_longlong(v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, 63);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), 63);
+    return __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
+}
+
+__device__ __forceinline__ void load_f32x8_planes(const float4 *lo, const float4 *hi, float (&m)[8]) {
+    const float4 a = *lo, b = *hi;
+    m[0] = a.x; m[1] = a.y; m[2] = a.z; m[3] = a.w;
+    m[4] = b.x; m[5] = b.y; m[6] = b.z; m[7] = b.w;
+}
+
+// NW waves per row; thread t holds column groups t + 64 NW i, i < ITS, and the
+// gamma and beta of its columns for all of the block's rows (row b, b + grid,
+// ...), the next row's elements in flight meanwhile.  The waves' sums meet in
+// LDS slots that alternate between rows: one barrier a row, none for NW = 1.
+template <int DT, int FMT, int NORM, bool HAS_BETA, int NW, int ITS, bool NT>
+__global__ __launch_bounds__(64 * NW) void mx_norm_kernel(const void *__restrict__ x, int64_t M,
+                                                          int64_t K,
+                                                          const float *__restrict__ gamma,
+                                                          const float *__restrict__ beta, float eps,
+                                                          uint8_t *__restrict__ q,
+                                                          uint8_t *__restrict__ scale) {
+    constexpr int T = 64 * NW;
+    __shared__ double red[2][2][NW];
     const int K8 = (int)(K >> 3);
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, wave = tid >> 6;
+    int col[ITS];  // (lanes past the row repeat its last block)
+    bool in[ITS];
+#pragma unroll
+    for (int i = 0; i < ITS; ++i) {
+        const int c = tid + T * i;
+        in[i] = c < K8;
+        col[i] = in[i] ? c : K8 - 4 + (tid & 3);
+    }
+    int64_t row = blockIdx.x;
     Raw8<DT> raw[ITS];
 #pragma unroll
+    for (int i = 0; i < ITS; ++i) raw[i] = load8<DT, NT>(x, row * K8 + col[i]);
+    float g[ITS][8], bt[HAS_BETA ? ITS : 1][8];
+#pragma unroll
     for (int i = 0; i < ITS; ++i) {
-        const int c = tid + 256 * i;
-        raw[i] = load8<DT, false>(x, row * K8 + (c < K8 ? c : K8 - 4 + (tid & 3)));
+        load_f32x8(gamma + col[i] * 8, g[i]);
+        if constexpr (HAS_BETA) load_f32x8(beta + col[i] * 8, bt[i]);
     }
-    const double pivot = NORM == 0 ? (double)first_of<DT>(x, row * K) : 0.0;
-    double s1 = 0.0, s2 = 0.0;
+    const double inv_k = 1.0 / (double)K;
+    // (the waves' totals of s1 and s2, in every lane)
+    auto total = [&](double &s1, double &s2, int par) __attribute__((always_inline)) {
+        if constexpr (NORM == 0) s1 = wave_sum_to_last(s1);
+        s2 = wave_sum_to_last(s2);
+        if constexpr (NW == 1) {
+            if constexpr (NORM == 0) s1 = of_lane63(s1);
+            s2 = of_lane63(s2);
+        } else {
+            if ((tid & 63) == 63) {
+                if constexpr (NORM == 0) red[par][0][wave] = s1;
+                red[par][1][wave] = s2;
+            }
+            __syncthreads();
+            s1 = 0.0;
+            s2 = 0.0;
 #pragma unroll
-    for (int i = 0; i < ITS; ++i) {
-        float v[8];
-        widen8<DT>(raw[i], v);
-        if (tid + 256 * i < K8) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const double d = (double)v[k] - pivot;
-                if constexpr (NORM == 0) s1 += d;
-                s2 = __builtin_fma(d, d, s2);
+            for (int w = 0; w < NW; ++w) {
+                if constexpr (NORM == 0) s1 += red[par][0][w];
+                s2 += red[par][1][w];
             }
         }
+    };
+    int par = 0;
+    // One row held in `cur`; the next row's loads go to `nxt` first.
+    auto one_row = [&](const Raw8<DT> (&cur)[ITS], Raw8<DT> (&nxt)[ITS]) __attribute__((always_inline)) {
+        const int64_t next = row + gridDim.x;
+        if (next < M) {
+#pragma unroll
+            for (int i = 0; i < ITS; ++i) nxt[i] = load8<DT, NT>(x, next * K8 + col[i]);
+        }
+        float v[ITS][8];
+        double s1 = 0.0, s2 = 0.0;
+#pragma unroll
+        for (int i = 0; i < ITS; ++i) {
+            widen8<DT>(cur[i], v[i]);
+            if (in[i]) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const double d = (double)v[i][k];
+                    if constexpr (NORM == 0) s1 += d;
+                    s2 = __builtin_fma(d, d, s2);
+                }
+            }
+        }
+        total(s1, s2, par);
+        par ^= 1;
+        const double mean = NORM == 0 ? s1 * inv_k : 0.0;
+        double var = s2 * inv_k - mean * mean;
+        if constexpr (NORM == 0) {
+            if (mean * mean > 256.0 * var) {  // (uniform over the row's waves)
+                double c1 = 0.0, c2 = 0.0;
+#pragma unroll
+                for (int i = 0; i < ITS; ++i)
+                    if (in[i]) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const double d = (double)v[i][k] - mean;
+                            c2 = __builtin_fma(d, d, c2);
+                        }
+                    }
+                total(c1, c2, par);
+                par ^= 1;
+                var = c2 * inv_k;
+            }
+        }
+        const float mu = (float)mean;
+        const float rstd = row_rstd(var + (double)eps);
+#pragma unroll
+        for (int i = 0; i < ITS; ++i) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                float y = v[i][k];
+                if constexpr (NORM == 0) y = y - mu;
+                y = y * rstd;
+                y = y * g[i][k];
+                if constexpr (HAS_BETA) y = y + bt[i][k];
+                v[i][k] = y;
+            }
+            uint32_t e;
+            const MxCodes<FMT> cd = mx_encode8<FMT>(v[i], e);
+            if (in[i]) mx_store8<FMT, NT>(q, scale, row * K8 + col[i], cd, e);
+        }
+        row = next;
+    };
+    Raw8<DT> other[ITS];
+    for (;;) {
+        one_row(raw, other);
+        if (row >= M) break;
+        one_row(other, raw);
+        if (row >= M) break;
     }
-    s1 = NORM == 0 ? wave_sum(s1) : 0.0;
-    s2 = wave_sum(s2);
-    if ((tid & 63) == 0) {
-        red[0][tid >> 6] = s1;
-        red[1][tid >> 6] = s2;
+}
+
+// Many rows of a 16-bit type with a beta, 4096 < K <= 8192: a wave per row and
+// no barrier, gamma and beta in LDS (four floats of a group's first half, then
+// of its second, so that successive lanes read successive 16 bytes).  With a
+// beta the kernel above holds 64 parameters a thread and two blocks a CU;
+// 16384 x 7168 fp16, layer norm to e2m1: 71 us here, 85 there (RMS norm 63 and
+// 65; without a beta 66 and 65, RMS 61 and 57: these stay there).  The row is
+// held as loaded and widened again for the output.
+template <int DT, int FMT, int NORM, int ITS>
+__global__ __launch_bounds__(512) void mx_norm_wave_kernel(const void *__restrict__ x, int64_t M,
+                                                           int64_t K,
+                                                           const float *__restrict__ gamma,
+                                                           const float *__restrict__ beta,
+                                                           float eps, uint8_t *__restrict__ q,
+                                                           uint8_t *__restrict__ scale) {
+    static_assert(DT != F32, "16-bit rows");
+    constexpr int KMAX8 = ITS * 64;
+    __shared__ float4 sg[2][KMAX8], sb[2][KMAX8];
+    const int K8 = (int)(K >> 3);
+    const int tid = threadIdx.x, lane = tid & 63;
+    for (int i = tid; i < 2 * K8; i += 512) {
+        sg[i & 1][i >> 1] = reinterpret_cast<const float4 *>(gamma)[i];
+        sb[i & 1][i >> 1] = reinterpret_cast<const float4 *>(beta)[i];
     }
     __syncthreads();
-    s1 = red[0][0] + red[0][1] + red[0][2] + red[0][3];
-    s2 = red[1][0] + red[1][1] + red[1][2] + red[1][3];
-    const double kd = (double)K;
-    const double dm = s1 / kd;
-    double var = s2 / kd - dm * dm;
-    var = var < 0.0 ? 0.0 : var;  // (rounding of a constant row; a NaN stays)
-    const float mu = (float)(pivot + dm);
-    const float rstd = (float)(1.0 / sqrt(var + (double)eps));
+    const double inv_k = 1.0 / (double)K;
+    for (int64_t row = (int64_t)blockIdx.x * 8 + (tid >> 6); row < M; row += (int64_t)gridDim.x * 8) {
+        Raw8<DT> raw[ITS];
 #pragma unroll
-    for (int i = 0; i < ITS; ++i) {
-        if (256 * i >= K8) break;
-        const int c = tid + 256 * i;
-        const bool in = c < K8;
-        const int cc = in ? c : K8 - 4 + (tid & 3);
-        float v[8], g[8], bt[8];
-        widen8<DT>(raw[i], v);
-        load_f32x8(gamma + cc * 8, g);
-        if constexpr (HAS_BETA) load_f32x8(beta + cc * 8, bt);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            if constexpr (NORM == 0) v[k] = v[k] - mu;
-            v[k] = v[k] * rstd;
-            v[k] = v[k] * g[k];
-            if constexpr (HAS_BETA) v[k] = v[k] + bt[k];
+        for (int i = 0; i < ITS; ++i) {
+            const int c = 64 * i + lane;  // (past the row: its last block again)
+            raw[i] = load8<DT, true>(x, row * K8 + (c < K8 ? c : K8 - 4 + (lane & 3)));
         }
-        uint32_t e;
-        const MxCodes<FMT> cd = mx_encode8<FMT>(v, e);
-        if (in) mx_store8<FMT, false>(q, scale, row * K8 + c, cd, e);
+        double s1 = 0.0, s2 = 0.0;
+#pragma unroll
+        for (int i = 0; i < ITS; ++i) {
+            if (64 * i + lane < K8) {
+                float v[8];
+                widen8<DT>(raw[i], v);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const double d = (double)v[k];
+                    if constexpr (NORM == 0) s1 += d;
+                    s2 = __builtin_fma(d, d, s2);
+                }
+            }
+        }
+        if constexpr (NORM == 0) s1 = of_lane63(wave_sum_to_last(s1));
+        s2 = of_lane63(wave_sum_to_last(s2));
+        const double mean = NORM == 0 ? s1 * inv_k : 0.0;
+        double var = s2 * inv_k - mean * mean;
+        if constexpr (NORM == 0) {
+            if (mean * mean > 256.0 * var) {
+                double c2 = 0.0;
+#pragma unroll
+                for (int i = 0; i < ITS; ++i) {
+                    if (64 * i + lane < K8) {
+                        float v[8];
+                        widen8<DT>(raw[i], v);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const double d = (double)v[k] - mean;
+                            c2 = __builtin_fma(d, d, c2);
+                        }
+                    }
+                }
+                var = of_lane63(wave_sum_to_last(c2)) * inv_k;
+            }
+        }
+        const float mu = (float)mean;
+        const float rstd = row_rstd(var + (double)eps);
+#pragma unroll
+        for (int i = 0; i < ITS; ++i) {
+            if (64 * i >= K8) break;
+            const int c = 64 * i + lane;
+            const bool in = c < K8;
+            const int cc = in ? c : K8 - 4 + (lane & 3);
+            float v[8], g[8], bt[8];
+            widen8<DT>(raw[i], v);
+            load_f32x8_planes(&sg[0][cc], &sg[1][cc], g);
+            load_f32x8_planes(&sb[0][cc], &sb[1][cc], bt);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                if constexpr (NORM == 0) v[k] = v[k] - mu;
+                v[k] = v[k] * rstd;
+                v[k] = v[k] * g[k];
+                v[k] = v[k] + bt[k];
+            }
+            uint32_t e;
+            const MxCodes<FMT> cd = mx_encode8<FMT>(v, e);
+            if (in) mx_store8<FMT, true>(q, scale, row * K8 + c, cd, e);
+        }
     }
+}
+
+template <int DT, int FMT, int NORM, bool HAS_BETA, int NW, int ITS>
+static void launch_mn_t(const void *x, int64_t M, int64_t K, const float *gamma, const float *beta,
+                        float eps, uint8_t *q, uint8_t *scale, hipStream_t stream) {
+    auto launch = [&](auto kernel) {
+        // As many blocks as the chip holds at once, so that all walk down the
+        // rows together (a second, partial round of blocks would double the
+        // time where the last round is short).
+        static const int64_t resident = [&] {
+            int n = 0;
+            if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, 64 * NW, 0) != hipSuccess || n < 1)
+                n = 1;
+            return (int64_t)n * 256;
+        }();
+        const dim3 grid((unsigned)(M < resident ? M : resident));
+        kernel<<<grid, 64 * NW, 0, stream>>>(x, M, K, gamma, beta, eps, q, scale);
+    };
+    if (M * K * dt_bytes(DT) > kNtLoadBytes) launch(mx_norm_kernel<DT, FMT, NORM, HAS_BETA, NW, ITS, true>);
+    else launch(mx_norm_kernel<DT, FMT, NORM, HAS_BETA, NW, ITS, false>);
 }
 
 template <int DT, int FMT, int NORM, bool HAS_BETA>
 static void launch_mn(const void *x, int64_t M, int64_t K, const float *gamma, const float *beta,
                       float eps, uint8_t *q, uint8_t *scale, hipStream_t stream) {
-    const dim3 grid((unsigned)M);
-    if (K <= 2048) mx_norm_kernel<DT, FMT, NORM, HAS_BETA, 1><<<grid, 256, 0, stream>>>(x, K, gamma, beta, eps, q, scale);
-    else if (K <= 4096) mx_norm_kernel<DT, FMT, NORM, HAS_BETA, 2><<<grid, 256, 0, stream>>>(x, K, gamma, beta, eps, q, scale);
-    else if (K <= 8192) mx_norm_kernel<DT, FMT, NORM, HAS_BETA, 4><<<grid, 256, 0, stream>>>(x, K, gamma, beta, eps, q, scale);
-    else mx_norm_kernel<DT, FMT, NORM, HAS_BETA, 8><<<grid, 256, 0, stream>>>(x, K, gamma, beta, eps, q, scale);
+    auto go = [&](auto nw, auto its) {
+        launch_mn_t<DT, FMT, NORM, HAS_BETA, decltype(nw)::value, decltype(its)::value>(
+            x, M, K, gamma, beta, eps, q, scale, stream);
+    };
+    using std::integral_constant;
+    constexpr integral_constant<int, 1> c1;
+    constexpr integral_constant<int, 2> c2;
+    constexpr integral_constant<int, 4> c4;
+    constexpr integral_constant<int, 8> c8;
+    if (M <= 512 && K > 512) {
+        // few rows: latency; a row spread over up to eight waves
+        if (K <= 2048) go(c4, c1);
+        else if (K <= 4096) go(c8, c1);
+        else if (K <= 8192) go(c8, c2);
+        else go(c8, c4);
+    } else if (DT != F32 && HAS_BETA && M >= 4096 && K > 4096 && K <= 8192) {
+        // (256 blocks of 8 rows: at least two rows a wave)
+        if constexpr (DT != F32 && HAS_BETA)
+            mx_norm_wave_kernel<DT, FMT, NORM, 16>
+                <<<256, 512, 0, stream>>>(x, M, K, gamma, beta, eps, q, scale);
+    } else {
+        // many rows: as few waves a row as hold it in four groups a thread
+        if (K <= 512) go(c1, c1);
+        else if (K <= 1024) go(c1, c2);
+        else if (K <= 2048) go(c1, c4);
+        else if (K <= 4096) go(c2, c4);
+        else if (K <= 8192) go(c4, c4);
+        else go(c8, c4);
+    }
 }
 
 template <int DT, int FMT>

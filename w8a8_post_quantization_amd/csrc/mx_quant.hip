@@ -110,97 +110,94 @@ void launch_quant_mx(const void *x, int dt, int64_t rows, int64_t K, const float
 
 // ------------------------------------------------------------------ inverse
 
-// y = value(code) 2^(e - 127): exact in fp32 (the conversion instruction
-// scales), then narrowed.  Rows are dense and hold whole blocks, so the
-// arrays are read flat: lane i takes the i-th group of eight elements.
-template <int FMT, int YDT>
-__device__ __forceinline__ void mx_decode8(const MxCodes<FMT> &c, uint32_t e, float (&v)[8]) {
+// y = value(code) 2^(e - 127), exact in fp32, then narrowed.  Rows are dense
+// and hold whole blocks, so the arrays are read flat: lane i takes the i-th
+// group of E elements, as many as make one 16-byte store.
+template <int FMT, int E>
+__device__ __forceinline__ void mx_decode(const uint32_t *c, uint32_t e, float (&v)[E]) {
     const float s = __uint_as_float(e > 0 ? (e == 255u ? 0x7fc00000u : e << 23) : 0x00400000u);
     typedef float f2 __attribute__((ext_vector_type(2)));
-    if constexpr (FMT == E2M1) {
-        const f2 p0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c.w[0], 1.0f, 0);
-        const f2 p1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c.w[0], 1.0f, 1);
-        const f2 p2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c.w[0], 1.0f, 2);
-        const f2 p3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c.w[0], 1.0f, 3);
-        v[0] = p0[0]; v[1] = p0[1]; v[2] = p1[0]; v[3] = p1[1];
-        v[4] = p2[0]; v[5] = p2[1]; v[6] = p3[0]; v[7] = p3[1];
-    } else {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const f2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.w[h], false);
-            const f2 hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.w[h], true);
-            v[4 * h] = lo[0]; v[4 * h + 1] = lo[1]; v[4 * h + 2] = hi[0]; v[4 * h + 3] = hi[1];
+    for (int h = 0; h < E / 4; ++h) {
+        f2 lo, hi;
+        if constexpr (FMT == E2M1) {  // (the byte of the word is an immediate)
+            lo = h == 0 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[0], 1.0f, 0)
+                        : __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[0], 1.0f, 2);
+            hi = h == 0 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[0], 1.0f, 1)
+                        : __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[0], 1.0f, 3);
+        } else {
+            lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)c[h], false);
+            hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)c[h], true);
         }
+        v[4 * h] = lo[0] * s;
+        v[4 * h + 1] = lo[1] * s;
+        v[4 * h + 2] = hi[0] * s;
+        v[4 * h + 3] = hi[1] * s;
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = v[i] * s;
 }
 
 template <int FMT, int YDT, bool NT>
 __global__ __launch_bounds__(256) void mx_dequant_kernel(const uint8_t *__restrict__ q,
                                                          const uint8_t *__restrict__ scale,
-                                                         int64_t n8, void *__restrict__ y) {
-    constexpr int U = 4;
+                                                         int64_t n, void *__restrict__ y) {
+    constexpr int U = 4, E = Vec<YDT>::n;  // groups in flight, elements a group
     using T = typename OutT<YDT>::T;
-    for (int64_t b = (int64_t)blockIdx.x * (256 * U); b < n8; b += (int64_t)gridDim.x * (256 * U)) {
-        MxCodes<FMT> c[U];
-        uint32_t e[U];
+    for (int64_t b = (int64_t)blockIdx.x * (256 * U); b < n; b += (int64_t)gridDim.x * (256 * U)) {
+        uint32_t c[U][2], e[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             int64_t i = b + u * 256 + threadIdx.x;
-            i = i < n8 ? i : n8 - 1;
-            if constexpr (FMT == E2M1) {
-                c[u].w[0] = reinterpret_cast<const uint32_t *>(q)[i];
-            } else {
+            i = i < n ? i : n - 1;
+            if constexpr (FMT == E2M1 && E == 4) {
+                c[u][0] = reinterpret_cast<const uint16_t *>(q)[i];
+            } else if constexpr (FMT == E4M3 && E == 8) {
                 const uint2 t = reinterpret_cast<const uint2 *>(q)[i];
-                c[u].w[0] = t.x;
-                c[u].w[1] = t.y;
+                c[u][0] = t.x;
+                c[u][1] = t.y;
+            } else {
+                c[u][0] = reinterpret_cast<const uint32_t *>(q)[i];
             }
-            e[u] = scale[i >> 2];
+            e[u] = scale[i / (32 / E)];
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t i = b + u * 256 + threadIdx.x;
-            if (i >= n8) break;
-            float v[8];
-            mx_decode8<FMT, YDT>(c[u], e[u], v);
-            T h[8];
+            if (i >= n) break;
+            float v[E];
+            mx_decode<FMT, E>(c[u], e[u], v);
+            T h[E];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) h[k] = narrow<YDT>(v[k]);
-            u4v *p = reinterpret_cast<u4v *>(y) + i * (YDT == F32 ? 2 : 1);
-#pragma unroll
-            for (int k = 0; k < (YDT == F32 ? 2 : 1); ++k) {
-                u4v w;
-                __builtin_memcpy(&w, reinterpret_cast<const char *>(h) + 16 * k, 16);
-                if constexpr (NT) __builtin_nontemporal_store(w, p + k);
-                else p[k] = w;
-            }
+            for (int k = 0; k < E; ++k) h[k] = narrow<YDT>(v[k]);
+            u4v *p = reinterpret_cast<u4v *>(y) + i;
+            const u4v w = __builtin_bit_cast(u4v, h);
+            if constexpr (NT) __builtin_nontemporal_store(w, p);
+            else *p = w;
         }
     }
 }
 
 template <int FMT, int YDT>
-static void launch_dq(const uint8_t *q, const uint8_t *scale, int64_t n8, void *y,
+static void launch_dq(const uint8_t *q, const uint8_t *scale, int64_t elems, void *y,
                       hipStream_t stream) {
-    const int64_t blocks = (n8 + 1023) / 1024;
+    const int64_t n = elems / Vec<YDT>::n, blocks = (n + 1023) / 1024;
     const dim3 grid((unsigned)(blocks < 4096 ? blocks : 4096));
-    if (n8 * 8 * dt_bytes(YDT) > kNtLoadBytes)
-        mx_dequant_kernel<FMT, YDT, true><<<grid, 256, 0, stream>>>(q, scale, n8, y);
+    if (elems * dt_bytes(YDT) > kNtLoadBytes)
+        mx_dequant_kernel<FMT, YDT, true><<<grid, 256, 0, stream>>>(q, scale, n, y);
     else
-        mx_dequant_kernel<FMT, YDT, false><<<grid, 256, 0, stream>>>(q, scale, n8, y);
+        mx_dequant_kernel<FMT, YDT, false><<<grid, 256, 0, stream>>>(q, scale, n, y);
 }
 
 void launch_dequant_mx(const uint8_t *q, const uint8_t *scale, int fmt, int64_t rows, int64_t K,
                        void *y, int y_dt, hipStream_t stream) {
-    const int64_t n8 = rows * (K / 8);
+    const int64_t n = rows * K;
     if (fmt == E2M1) {
-        if (y_dt == F32) launch_dq<E2M1, F32>(q, scale, n8, y, stream);
-        else if (y_dt == F16) launch_dq<E2M1, F16>(q, scale, n8, y, stream);
-        else launch_dq<E2M1, BF16>(q, scale, n8, y, stream);
+        if (y_dt == F32) launch_dq<E2M1, F32>(q, scale, n, y, stream);
+        else if (y_dt == F16) launch_dq<E2M1, F16>(q, scale, n, y, stream);
+        else launch_dq<E2M1, BF16>(q, scale, n, y, stream);
     } else {
-        if (y_dt == F32) launch_dq<E4M3, F32>(q, scale, n8, y, stream);
-        else if (y_dt == F16) launch_dq<E4M3, F16>(q, scale, n8, y, stream);
-        else launch_dq<E4M3, BF16>(q, scale, n8, y, stream);
+        if (y_dt == F32) launch_dq<E4M3, F32>(q, scale, n, y, stream);
+        else if (y_dt == F16) launch_dq<E4M3, F16>(q, scale, n, y, stream);
+        else launch_dq<E4M3, BF16>(q, scale, n, y, stream);
     }
 }
 

@@ -60,43 +60,6 @@ __device__ __forceinline__ void norm_stats(int64_t S1, u128 S2, int64_t K, float
     rstd = (float)(1.0 / sqrt(var + (double)eps));
 }
 
-// Wave sums and maxima through DPP lane moves (no LDS round trip): four
-// steps leave each 16-lane row's total in all its lanes, two row broadcasts
-// then carry the wave's total into lane 63.
-template <int CTRL, int ROWS>
-__device__ __forceinline__ int dpp_i32(int v) {
-    if constexpr (ROWS == 0xf) return __builtin_amdgcn_mov_dpp(v, CTRL, 0xf, 0xf, false);
-    else return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xf, false);  // other rows: 0
-}
-template <int CTRL, int ROWS>
-__device__ __forceinline__ double dpp_f64(double v) {
-    const uint64_t u = (uint64_t)__double_as_longlong(v);
-    const uint32_t lo = (uint32_t)dpp_i32<CTRL, ROWS>((int)(uint32_t)u);
-    const uint32_t hi = (uint32_t)dpp_i32<CTRL, ROWS>((int)(uint32_t)(u >> 32));
-    return __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
-}
-// quad_perm [1,0,3,2], quad_perm [2,3,0,1], row_half_mirror, row_mirror,
-// row_bcast:15 into rows 1 and 3, row_bcast:31 into rows 2 and 3.
-__device__ __forceinline__ double wave_sum_to_last(double v) {
-    v += dpp_f64<0xb1, 0xf>(v);
-    v += dpp_f64<0x4e, 0xf>(v);
-    v += dpp_f64<0x141, 0xf>(v);
-    v += dpp_f64<0x140, 0xf>(v);
-    v += dpp_f64<0x142, 0xa>(v);
-    v += dpp_f64<0x143, 0xc>(v);
-    return v;
-}
-// Non-negative inputs: lanes outside a broadcast's rows read 0.
-__device__ __forceinline__ float wave_max_to_last(float v) {
-    v = fmaxf(v, __int_as_float(dpp_i32<0xb1, 0xf>(__float_as_int(v))));
-    v = fmaxf(v, __int_as_float(dpp_i32<0x4e, 0xf>(__float_as_int(v))));
-    v = fmaxf(v, __int_as_float(dpp_i32<0x141, 0xf>(__float_as_int(v))));
-    v = fmaxf(v, __int_as_float(dpp_i32<0x140, 0xf>(__float_as_int(v))));
-    v = fmaxf(v, __int_as_float(dpp_i32<0x142, 0xa>(__float_as_int(v))));
-    v = fmaxf(v, __int_as_float(dpp_i32<0x143, 0xc>(__float_as_int(v))));
-    return v;
-}
-
 // The low bytes of eight words, in order, as two words: perm's selector
 // 0x0c0c0400 takes [b0 of the second operand, b0 of the first, 0, 0], and
 // 0x05040100 joins two such halves.
