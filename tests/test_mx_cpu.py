@@ -180,7 +180,7 @@ def test_gemm_validation():
     assert call(y=FAKE + 2) == ALIGN
     assert call(M=0, x=None, y=None) == OK and call(N=0, w=None, y=None) == OK
     assert call(K=(1 << 20) + 32) == UNSUP
-    for bad in (-2, 3):
+    for bad in (-2, 4):
         assert sq.lib().sq_gemm_mxfp4_tile(FAKE, FAKE, 0, FAKE, FAKE, 64, 64, 256, FAKE, sq.SQ_F32,
                                            None, bad) == ARG
 

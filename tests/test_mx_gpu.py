@@ -310,13 +310,15 @@ def test_product_parity(torch, M, N, K, ydt, spread, fmt):
 
 
 @pytest.mark.parametrize("fmt", ["e2m1", "e4m3"])
-@pytest.mark.parametrize("tile", [0, 1, 2])
+@pytest.mark.parametrize("tile", [0, 1, 2, 3])
 @pytest.mark.parametrize("M,N,K,ydt", [
     (40, 100, 256, "f32"), (300, 333, 384, "bf16"), (513, 520, 512, "f32"), (33, 260, 640, "f16"),
-    (129, 1030, 1152, "f32"), (256, 256, 1280, "bf16"), (700, 130, 4224, "f32")])
+    (129, 1030, 1152, "f32"), (256, 256, 1280, "bf16"), (700, 130, 4224, "f32"),
+    (200, 300, 288, "f32"), (65, 129, 800, "bf16"), (140, 270, 1056, "f16"), (300, 200, 2272, "f32")])
 def test_product_tiles(torch, M, N, K, ydt, tile, fmt):
     """Every block shape of the pipelined kernel: fewer stages than its ring,
-    as many and more, with and without a last half stage, ragged edges."""
+    as many and more, with and without a last partial stage, scale rows that
+    start at any byte (K % 128 != 0), ragged edges."""
     f = FMT[fmt]
     xq, xs = _codes(M * 7 + K, M, K, f, 1)
     if f == ref.E4M3:

@@ -128,7 +128,11 @@ __device__ __forceinline__ void mx_epilogue(const MxArgs &p,
             if (m >= M || n >= N) continue;
             T *yp = reinterpret_cast<T *>(p.y) + (int64_t)m * N + n;
             if (n + EPC <= N) {
-                *reinterpret_cast<uint4 *>(yp) = v;
+                // 16-bit outputs past the caches (4096 x 14336 x 4096: 130 us
+                // against 136; fp32 ones measured 23.1 us so, 22.5 not)
+                if constexpr (sizeof(T) == 2)
+                    __builtin_nontemporal_store(__builtin_bit_cast(u4v, v), reinterpret_cast<u4v *>(yp));
+                else *reinterpret_cast<uint4 *>(yp) = v;
             } else {
                 T e[EPC];
                 __builtin_memcpy(e, &v, 16);
@@ -160,7 +164,7 @@ __device__ __forceinline__ void mx_sched() {
 // 128 (e2m1) or twice 128 (e4m3, two half tiles) of every activation row,
 // streamed into a ring of STA LDS stages by direct-to-LDS loads, with chunk c
 // of a 128-byte row r at slot c ^ swz(r).  It is consumed as four quarters of
-// 64 elements with ping-pong fragment registers.
+// 64 elements.
 //
 // Which blocks of a stage meet in a quarter is free as long as both operands
 // agree: lane half h takes block 4 h + q in quarter q, so a lane's four scale
@@ -196,7 +200,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx_gemm_pp(MxArgs p) {
     static_assert(CH == 0 || CH == 2 || CH == 4, "stages per scale load");
     static_assert(REGS || (LS * RPS * NW == BM + BN && BM % RPS == 0 && STA <= CH + 1), "scale loads");
     static_assert(STA >= 2 && STA * L + 2 * LS < 64, "vmcnt range");
-    static_assert(!REGS || (BM + BN == 64 * NW && STA == 2), "one scale row per thread");
+    static_assert(!REGS || (BM + BN <= 64 * NW && STA == 2), "a thread per scale row");
     static_assert(NW * 32 * WTN * 4 <= STA * STG, "slabs");
     __shared__ __attribute__((aligned(1024))) uint8_t smem[STA * STG + SS];
     uint8_t *const sscale = smem + STA * STG;
@@ -234,8 +238,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx_gemm_pp(MxArgs p) {
     const uint8_t *xq0 = p.xq + (int64_t)m0 * (K * (int64_t)XH / 2), *wq0 = p.wq + (int64_t)n0 * (K / 2);
     const uint8_t *s_row = nullptr;  // REGS: this thread's scale row
     if constexpr (REGS) {
-        s_row = tid < BM ? xs0 + (int64_t)(tid < mtop ? tid : mtop) * KB
-                         : ws0 + (int64_t)(tid - BM < ntop ? tid - BM : ntop) * KB;
+        const int t = tid < BM + BN ? tid : BM + BN - 1;  // (spare threads repeat the last row)
+        s_row = t < BM ? xs0 + (int64_t)(t < mtop ? t : mtop) * KB
+                       : ws0 + (int64_t)(t - BM < ntop ? t - BM : ntop) * KB;
     }
     uint2 rs = make_uint2(0, 0);
     auto issue = [&](int s) __attribute__((always_inline)) {  // stage s < nk
@@ -360,7 +365,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx_gemm_pp(MxArgs p) {
     };
     // Where stage s has landed in this wave: its scale rows go to LDS too.
     auto publish_scales = [&](int s) {
-        if constexpr (REGS) *reinterpret_cast<uint2 *>(sscale + (s & 1) * ((BM + BN) * 8) + tid * 8) = rs;
+        if constexpr (REGS) {
+            const int t = tid < BM + BN ? tid : BM + BN - 1;
+            *reinterpret_cast<uint2 *>(sscale + (s & 1) * ((BM + BN) * 8) + t * 8) = rs;
+        }
     };
     constexpr std::integral_constant<int, 0> q0;
     constexpr std::integral_constant<int, 1> q1;
@@ -376,6 +384,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx_gemm_pp(MxArgs p) {
         if (s < nk) issue(s);
     wait_stages<STA - 1, L + (REGS ? 1 : 0)>((nk < STA ? nk : STA) - 1);  // stage 0 landed
     lds_barrier();
+    // (Fragments are read one quarter before they multiply; two quarters, with
+    // four sets of registers, measured no faster at any shape.)
     XFrag<XF> xa[FM], xb[FM];
     int4v wa[FN], wb[FN];
     read_scales(0);
@@ -789,30 +799,43 @@ template <int XF>
 static void launch_mx(MxArgs &a, int y_dt, hipStream_t stream, int tile) {
     if (a.M <= 16) return launch_dec<XF, 1>(a, y_dt, stream);
     if (a.M <= 32 || a.K < 256) return launch_dec<XF, 2>(a, y_dt, stream);
-    if (a.K % 128 != 0) return launch_pp<XF, 128, 128, 2, 2, 2, 0>(a, stream);
+    if (a.K % 128 != 0) {
+        if (tile < 3) launch_pp<XF, 128, 128, 2, 2, 2, 0>(a, stream);
+        else launch_pp<XF, 64, 128, 2, 2, 2, 0>(a, stream);
+        return;
+    }
     if constexpr (XF == E2M1) {
         if (tile == 0) launch_pp<XF, 256, 256, 4, 2, 2, 2>(a, stream);
         else if (tile == 1) launch_pp<XF, 256, 128, 4, 2, 3, 4>(a, stream);
-        else launch_pp<XF, 128, 128, 2, 2, 2, 4>(a, stream);
+        else if (tile == 2) launch_pp<XF, 128, 128, 2, 2, 2, 4>(a, stream);
+        else launch_pp<XF, 64, 128, 2, 2, 2, 4>(a, stream);
     } else {
         if (tile == 0) launch_pp<XF, 128, 256, 2, 4, 2, 4>(a, stream);
-        else launch_pp<XF, 128, 128, 2, 2, 2, 4>(a, stream);
+        else if (tile < 3) launch_pp<XF, 128, 128, 2, 2, 2, 4>(a, stream);
+        else launch_pp<XF, 64, 128, 2, 2, 2, 4>(a, stream);
     }
 }
 
-// The block tile of M > 32: the largest whose tiles fill the 256 CUs best.
-static int mx_pick_tile(int x_fmt, int64_t M, int64_t N) {
-    struct C { int bm, bn; double eff; int per_cu; };
-    const C e2[3] = {{256, 256, 1.0, 1}, {256, 128, 0.85, 1}, {128, 128, 0.7, 2}};
-    const C e4[2] = {{128, 256, 1.0, 1}, {128, 128, 0.7, 1}};
-    const C *c = x_fmt == E2M1 ? e2 : e4;
+// The block tile of M > 32: the least rounds of tiles over the 256 CUs, each
+// taking its outputs over the shape's rate.  The rates are relative to the
+// largest shape's, from these times (us; tiles as numbered in launch_mx):
+//   e2m1  4096 x 4096 x 1024 (fp16)   17.4  19.1  18.9
+//         2048 x 4096 x 4096          29.4  23.4  25.3
+//         4096 x 1024 x 1024          11.6   9.0   7.8
+//         256 x 28672 x 7168          62.6  42.5  44.1
+//   e4m3  4096 x 4096 x 1024          24.7   -    34.6
+//         2048 x 4096 x 4096          32.9   -    50.5
+static int mx_pick_tile(int x_fmt, int64_t M, int64_t N, int64_t K) {
+    struct C { int bm, bn; double rate; };
+    const C e2[4] = {{256, 256, 1.0}, {256, 128, 0.85}, {128, 128, 0.7}, {64, 128, 0.5}};
+    const C e4[4] = {{128, 256, 1.0}, {128, 128, 0.7}, {128, 128, 0.7}, {64, 128, 0.5}};
     int best = 0;
-    double best_score = -1;
-    for (int i = 0; i < (x_fmt == E2M1 ? 3 : 2); ++i) {
-        const int64_t tiles = ((M + c[i].bm - 1) / c[i].bm) * ((N + c[i].bn - 1) / c[i].bn);
-        const int64_t slots = 256 * c[i].per_cu, rounds = (tiles + slots - 1) / slots;
-        const double score = (double)tiles / (double)(rounds * slots) * c[i].eff;
-        if (score > best_score + 1e-9) { best_score = score; best = i; }
+    double least = 0;
+    for (int i = K % 128 != 0 ? 2 : 0; i < 4; ++i) {
+        const C &c = x_fmt == E2M1 ? e2[i] : e4[i];
+        const int64_t tiles = ((M + c.bm - 1) / c.bm) * ((N + c.bn - 1) / c.bn);
+        const double t = (double)((tiles + 255) / 256) * c.bm * c.bn / c.rate;
+        if (least == 0 || t < least * 0.999) { least = t; best = i; }
     }
     return best;
 }
@@ -823,7 +846,7 @@ void launch_gemm_mx(const uint8_t *xq, const uint8_t *xs, int x_fmt, const uint8
     MxArgs a{};
     a.xq = xq; a.xs = xs; a.wq = wq; a.ws = ws;
     a.M = (int)M; a.N = (int)N; a.K = (int)K; a.y = y; a.y_dt = y_dt;
-    const int tile = force_tile >= 0 ? force_tile : mx_pick_tile(x_fmt, M, N);
+    const int tile = force_tile >= 0 ? force_tile : mx_pick_tile(x_fmt, M, N, K);
     if (x_fmt == E2M1) launch_mx<E2M1>(a, y_dt, stream, tile);
     else launch_mx<E4M3>(a, y_dt, stream, tile);
 }

@@ -181,7 +181,7 @@ __global__ __launch_bounds__(64 * NW) void mx_norm_kernel(const void *__restrict
 // no barrier, gamma and beta in LDS (four floats of a group's first half, then
 // of its second, so that successive lanes read successive 16 bytes).  With a
 // beta the kernel above holds 64 parameters a thread and two blocks a CU;
-// 16384 x 7168 fp16, layer norm to e2m1: 71 us here, 85 there (RMS norm 63 and
+// 16384 x 7168 fp16, layer norm to e2m1: 77 us here, 85 there (RMS norm 63 and
 // 65; without a beta 66 and 65, RMS 61 and 57: these stay there).  The row is
 // held as loaded and widened again for the output.
 template <int DT, int FMT, int NORM, int ITS>

@@ -91,7 +91,7 @@ int sq_dequantize_mx(const uint8_t *q, const uint8_t *scale, int fmt, int64_t ro
 int sq_gemm_mxfp4_tile(const uint8_t *xq, const uint8_t *x_scale, int x_fmt, const uint8_t *wq,
                        const uint8_t *w_scale, int64_t M, int64_t N, int64_t K, void *y, int y_dt,
                        void *stream, int tile) {
-    if (tile < -1 || tile > 2) return SQ_ERR_ARG;
+    if (tile < -1 || tile > 3) return SQ_ERR_ARG;
     if (!valid_dt(y_dt)) return SQ_ERR_DTYPE;
     if (!valid_fmt(x_fmt)) return SQ_ERR_ARG;
     if (bad_rows(M, K) || N < 0 || N > kMaxDim) return SQ_ERR_SHAPE;
