@@ -106,10 +106,10 @@ __device__ __forceinline__ void mx_epilogue(const MxArgs &p,
             }
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // slab written (one wave)
         if (!vec_y) {
-            // rows that start anywhere: 64 successive outputs of a row a store
+            // rows that start anywhere: successive lanes store successive outputs
 #pragma unroll 8
-            for (int k = 0; k < 32 * (WTN / 64); ++k) {
-                const int r = k / (WTN / 64), nl = (k % (WTN / 64)) * 64 + lane;
+            for (int k = 0; k < 32 * WTN / 64; ++k) {
+                const int i = k * 64 + lane, r = i / WTN, nl = i % WTN;
                 const int cb = nl * (int)sizeof(T);
                 const T v = *reinterpret_cast<const T *>(
                     slab + r * RB + (((cb >> 4) ^ ((r / RPW) & (CPR - 1))) << 4) + (cb & 15));
@@ -800,19 +800,19 @@ static void launch_mx(MxArgs &a, int y_dt, hipStream_t stream, int tile) {
     if (a.M <= 16) return launch_dec<XF, 1>(a, y_dt, stream);
     if (a.M <= 32 || a.K < 256) return launch_dec<XF, 2>(a, y_dt, stream);
     if (a.K % 128 != 0) {
-        if (tile < 3) launch_pp<XF, 128, 128, 2, 2, 2, 0>(a, stream);
-        else launch_pp<XF, 64, 128, 2, 2, 2, 0>(a, stream);
+        if (tile < 3) launch_pp<XF, 128, 128, 2, 4, 2, 0>(a, stream);
+        else launch_pp<XF, 64, 128, 2, 4, 2, 0>(a, stream);
         return;
     }
     if constexpr (XF == E2M1) {
         if (tile == 0) launch_pp<XF, 256, 256, 4, 2, 2, 2>(a, stream);
         else if (tile == 1) launch_pp<XF, 256, 128, 4, 2, 3, 4>(a, stream);
         else if (tile == 2) launch_pp<XF, 128, 128, 2, 2, 2, 4>(a, stream);
-        else launch_pp<XF, 64, 128, 2, 2, 2, 4>(a, stream);
+        else launch_pp<XF, 64, 128, 2, 4, 3, 4>(a, stream);
     } else {
         if (tile == 0) launch_pp<XF, 128, 256, 2, 4, 2, 4>(a, stream);
-        else if (tile < 3) launch_pp<XF, 128, 128, 2, 2, 2, 4>(a, stream);
-        else launch_pp<XF, 64, 128, 2, 2, 2, 4>(a, stream);
+        else if (tile < 3) launch_pp<XF, 128, 128, 4, 2, 3, 4>(a, stream);
+        else launch_pp<XF, 64, 128, 2, 4, 3, 4>(a, stream);
     }
 }
 
