@@ -25,7 +25,12 @@ weight side is unaffected under per-input-row quantization; with the
 per-output-channel weights used here w_err does grow with alpha, which is
 the trade-off the sweep shows.
 
-    python alpha_sweep.py [--config prefill_30b] [--mode static|token]
+The modes mxfp8 and mxfp4 run the microscaled path instead: weights in e2m1,
+activations in e4m3 or e2m1, a power-of-two scale for each 32 input channels;
+the same columns, without the outlier ratios' effect on a row step (a block's
+outlier costs its own block only), so alpha matters less there.
+
+    python alpha_sweep.py [--config prefill_30b] [--mode static|token|mxfp8|mxfp4]
                           [--alphas 0,0.1,...,1] [--rows 256]
 """
 from __future__ import annotations
@@ -39,6 +44,7 @@ import numpy as np
 import synth
 
 STATIC, TOKEN = "static", "token"
+MXFP8, MXFP4 = "mxfp8", "mxfp4"
 
 
 class GpuBackend:
@@ -90,6 +96,15 @@ class GpuBackend:
 
     def gemm(self, xq, wq, xs, ws):
         return self._h(self.sq.gemm_i8_dequant(xq, wq, xs, ws, out_dtype=self.torch.float32))
+
+    def mx_layer(self, x, w, s, inv_s, mode):
+        """(y, the values of X's codes, of W's codes) of the microscaled path."""
+        sq, f32 = self.sq, self.torch.float32
+        fmt = sq.SQ_MX_E4M3 if mode == MXFP8 else sq.SQ_MX_E2M1
+        wq = sq.smooth_weights_mxfp4(self._d(w), None if s is None else self._d(s))
+        xq = sq.quantize_act_mx(self._d(x), None if inv_s is None else self._d(inv_s), fmt)
+        return (sq.gemm_mxfp4(*xq, *wq, fmt, out_dtype=f32), sq.dequantize_mx(*xq, fmt),
+                sq.dequantize_mx(*wq))
 
     def rows(self, t, idx):
         if isinstance(t, np.ndarray):
@@ -161,6 +176,37 @@ def sweep(X, W, alphas, mode, backend, sample_rows=256, seed=0, X_cal=None):
     return out
 
 
+def mx_sweep(X, W, alphas, mode, backend, sample_rows=256, seed=0, X_cal=None):
+    """sweep() for the microscaled path (mode MXFP8 or MXFP4: the activations'
+    format): rows of the same keys."""
+    M, N = X.shape[0], W.shape[0]
+    rng = np.random.default_rng(seed)
+    xr = np.sort(rng.choice(M, size=min(M, sample_rows), replace=False))
+    wr = np.sort(rng.choice(N, size=min(N, 4 * sample_rows), replace=False))
+    X64, W64 = _f64(X), _f64(W)
+    ref = X64[xr] @ W64.T
+    x_amax = backend.absmax(X if X_cal is None else X_cal)
+    w_amax = backend.absmax(W)
+    out = []
+    for a in alphas:
+        s, inv_s = (None, None) if a is None else backend.scales(x_amax, w_amax, a, False)[:2]
+        s_eff = np.ones(X.shape[1]) if a is None else s.astype(np.float64)
+        y, xv, wv = backend.mx_layer(X, W, s, inv_s, mode)
+        xv = backend.rows(xv, xr).astype(np.float64)
+        wv = backend.rows(wv, wr).astype(np.float64)
+        out.append({
+            "alpha": "none" if a is None else round(float(a), 3),
+            "y_err": _rel(backend.rows(y, xr).astype(np.float64), ref),
+            "x_err": _rel(xv * s_eff[None, :], X64[xr]),
+            "w_err": _rel(wv / s_eff[None, :], W64[wr]),
+            "x_zero": float((xv == 0).mean()),
+            "w_zero": float((wv == 0).mean()),
+            "x_ratio": _ratio(x_amax / s_eff),
+            "w_ratio": _ratio(w_amax * s_eff),
+        })
+    return out
+
+
 CONFIGS = {
     "single_1024": lambda: synth.single_1024(),
     "prefill_30b": lambda: synth.prefill_30b(),
@@ -210,7 +256,7 @@ def markdown(rows, title):
 def main(argv=None):
     ap = argparse.ArgumentParser(description=__doc__.split("\n\n")[0])
     ap.add_argument("--config", default="all", choices=["all", *CONFIGS])
-    ap.add_argument("--mode", default="both", choices=["both", STATIC, TOKEN])
+    ap.add_argument("--mode", default="both", choices=["both", STATIC, TOKEN, MXFP8, MXFP4])
     ap.add_argument("--alphas", default="0,0.1,0.2,0.3,0.4,0.5,0.6,0.7,0.8,0.9,1")
     ap.add_argument("--rows", type=int, default=256)
     ap.add_argument("--json", action="store_true", help="one JSON line per table")
@@ -222,14 +268,17 @@ def main(argv=None):
     for name in names:
         cfg = CONFIGS[name]()
         for mode in modes:
-            rows = sweep(cfg["X"], cfg["W"], alphas, mode, backend, args.rows,
-                         X_cal=cfg.get("X_cal"))
-            title = f"{name}, X {'per-tensor static' if mode == STATIC else 'per-token'}"
+            run = mx_sweep if mode in (MXFP8, MXFP4) else sweep
+            rows = run(cfg["X"], cfg["W"], alphas, mode, backend, args.rows,
+                       X_cal=cfg.get("X_cal"))
+            how = {STATIC: "per-tensor static", TOKEN: "per-token", MXFP8: "e4m3 in blocks, W e2m1",
+                   MXFP4: "e2m1 in blocks, W e2m1"}[mode]
+            title = f"{name}, X {how}"
             if args.json:
                 print(json.dumps({"config": name, "mode": mode, "rows": rows}))
             else:
                 print(markdown(rows, title) + "\n", flush=True)
-    if args.config == "all":
+    if args.config == "all" and args.mode not in (MXFP8, MXFP4):
         cfg = synth.llm_int8_2048()
         rows = mixed_errors(cfg["X"], cfg["W"], [float("inf"), 6.0], backend, args.rows)
         if args.json:
