@@ -107,7 +107,9 @@ int sq_dequantize_mx(const uint8_t *q, const uint8_t *scale, int fmt, int64_t ro
  * on M, N and K, so a row's bits may depend on M.  A term of a block is
  * rounded to no worse than 2^-20 (e2m1) or 2^-9 (e4m3) of the largest term
  * of the instruction that adds it, then once to fp32 for each addition.
- * K % 32 == 0, 32 <= K <= 1048576 when M, N > 0 (SQ_ERR_UNSUPPORTED above).
+ * K % 32 == 0, 32 <= K <= 1048576 when M, N > 0 (SQ_ERR_UNSUPPORTED above);
+ * M, N <= 2^31 - 1024, in fewer tiles than 2^23 (SQ_ERR_UNSUPPORTED; a tile
+ * is 64 x 128 outputs at the least, 32 x 16 for K < 256).
  */
 int sq_gemm_mxfp4(const uint8_t *xq, const uint8_t *x_scale, int x_fmt, const uint8_t *wq,
                   const uint8_t *w_scale, int64_t M, int64_t N, int64_t K, void *y, int y_dt,

@@ -173,6 +173,10 @@ def test_gemm_validation():
     assert call(dt=9) == DTYPE and call(fmt=2) == ARG
     assert call(K=48) == SHAPE and call(M=-1) == SHAPE and call(N=-1) == SHAPE
     assert call(K=0) == SHAPE and call(N=1 << 31) == SHAPE
+    assert call(M=(1 << 31) - 1) == SHAPE and call(N=(1 << 31) - 1023) == SHAPE
+    # tiles past a grid's 2^32 threads: slabs of 32 rows, and tiles of 64 to 256
+    assert call(M=(1 << 31) - 1024, K=32) == UNSUP
+    assert call(M=(1 << 31) - 1024, N=4096, K=256) == UNSUP
     for name in ("x", "xs", "w", "ws", "y"):
         assert call(**{name: None}) == NULL, name
     assert call(x=FAKE + 8) == ALIGN and call(w=FAKE + 8) == ALIGN

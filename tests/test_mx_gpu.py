@@ -253,6 +253,25 @@ def test_norm_rows_that_are_not_finite(torch):
         assert_bits_equal(host(q1, torch)[r], host(q0, torch)[r], "codes of a finite row")
 
 
+@pytest.mark.parametrize("M", [5, 700])
+def test_rms_rows_with_an_infinity(torch, M):
+    """sigma^2 is infinite and rstd 0: an infinity's block is NaN (inf * 0), the
+    row's other elements are beta."""
+    K = 1056
+    x = synth.normal(4, 1, (M, K)).astype(np.float32)
+    x[2, 700], x[4, 33], x[4, 64] = np.inf, -np.inf, np.inf
+    g, b = np.ones(K, np.float32), np.linspace(-3, 5, K).astype(np.float32)
+    log(f"norm_quantize_act_mx RMS with infinities M={M}")
+    for beta in (None, b):
+        q, e = sq.norm_quantize_act_mx(dev(x, torch), dev(g, torch), None if beta is None else dev(b, torch),
+                                       sq.SQ_NORM_RMS, 1e-5)
+        with np.errstate(invalid="ignore"):
+            q_o, e_o = ref.quantize(ref.norm(x, g, beta, False, 1e-5), ref.E2M1)
+        assert (e_o[2] == 255).sum() == 1 and (e_o[4] == 255).sum() == 2
+        assert_bits_equal(host(e, torch), e_o, "x_scale")
+        assert_bits_equal(host(q, torch), q_o, "xq")
+
+
 # -------------------------------------------------------------------- product
 
 UNIT = {ref.E2M1: 2.0 ** -20, ref.E4M3: 2.0 ** -9}
@@ -473,6 +492,96 @@ def test_layer_eager_stream_and_graph(torch, M, fmt):
         for t, u, w in zip(outs, again, want):
             assert_bits_equal(hst(t), w, f"replay {r}")
             assert_bits_equal(hst(u), w, f"eager beside replay {r}")
+
+
+def test_first_call_inside_a_capture(torch):
+    """A variant that nothing before has launched (and whose grid size is asked
+    of the runtime on its first call) captured before it ever ran eagerly."""
+    M, K = 700, 2080
+    x = dev(_cast(synth.normal(41, 1, (M, K)).astype(np.float32), "bf16"), torch)
+    g = torch.rand(K, device="cuda") + 0.5
+    b = torch.rand(K, device="cuda") - 0.5
+    out = (torch.zeros((M, K), dtype=torch.uint8, device="cuda"),
+           torch.zeros((M, K // 32), dtype=torch.uint8, device="cuda"))
+    log("norm_quantize_act_mx first called in a capture")
+    s = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        sq.norm_quantize_act_mx(x, g, b, sq.SQ_NORM_RMS, 1e-5, sq.SQ_MX_E4M3, out=out)
+    q_o, e_o = ref.quantize(ref.norm(host(x, torch), host(g, torch), host(b, torch), False, 1e-5), ref.E4M3)
+    for _ in range(3):
+        out[0].zero_(), out[1].zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert_bits_equal(host(out[1], torch), e_o, "x_scale")
+        assert_bits_equal(host(out[0], torch), q_o, "xq")
+
+
+def test_two_streams_at_once(torch):
+    """No call has state of its own: the same and other calls interleaved on two
+    streams give each the bits they give alone."""
+    f = sq.SQ_MX_E4M3
+    runs = [_layer(torch, M, 512, 800, f, M)[0] for M in (7, 200)]
+    want = [[host(t, torch).copy() for t in run()] for run in runs]
+    streams = [torch.cuda.Stream() for _ in runs]
+    torch.cuda.synchronize()
+    log("two streams at once")
+    got = [[], []]
+    for _ in range(5):
+        for i, (run, s) in enumerate(zip(runs, streams)):
+            with torch.cuda.stream(s):
+                got[i].append(run())
+    torch.cuda.synchronize()
+    for i in range(2):
+        for outs in got[i]:
+            for t, w in zip(outs, want[i]):
+                assert_bits_equal(host(t, torch), w, f"stream {i}")
+
+
+@pytest.mark.parametrize("fmt", ["e2m1", "e4m3"])
+def test_short_inner_length_many_rows(torch, fmt):
+    """K < 256 takes slabs of 32 tokens: more of them than a grid's second
+    dimension could count."""
+    f = FMT[fmt]
+    M, N, K = 65536 * 32 + 5, 3, 32
+    xq, xs = _codes(77, M, K, f, 1)
+    wq, ws = _codes(78, N, K, ref.E2M1, 1)
+    log(f"gemm_mxfp4 M={M} N={N} K={K} {fmt}")
+    y = host(sq.gemm_mxfp4(*[dev(a, torch) for a in (xq, xs, wq, ws)], f, out_dtype=torch.float32), torch)
+    rows = np.r_[0:100, M - 100:M, np.random.default_rng(1).integers(0, M, 500)]
+    _check_product(y[rows], "f32", xq[rows], xs[rows], f, wq, ws)
+
+
+def test_past_four_gigabytes(torch):
+    """Codes, values and outputs whose offsets pass 2^32 bytes: the last rows
+    against their plain forms."""
+    K, M = 8192, 270000                       # bf16 x: 4.4 GB, e4m3 codes 2.2 GB
+    log(f"quantize and decode M={M} K={K}")
+    x = torch.zeros((M, K), dtype=torch.bfloat16, device="cuda")
+    tail = dev(_acts(90, 64, K, "bf16"), torch)
+    x[-64:] = tail
+    q, e = sq.quantize_act_mx(x, None, sq.SQ_MX_E4M3)
+    q_o, e_o = ref.quantize(ref.smoothed(host(tail, torch)), ref.E4M3)
+    assert_bits_equal(host(q[-64:], torch), q_o, "codes")
+    assert_bits_equal(host(e[-64:], torch), e_o, "scales")
+    y = sq.dequantize_mx(q, e, sq.SQ_MX_E4M3, out_dtype=torch.bfloat16)
+    want = sq.dequantize_mx(q[-64:].contiguous(), e[-64:].contiguous(), sq.SQ_MX_E4M3,
+                            out_dtype=torch.bfloat16)
+    assert torch.equal(y[-64:].view(torch.int16), want.view(torch.int16))
+    nq, ne = sq.norm_quantize_act_mx(x, torch.ones(K, device="cuda"), None, sq.SQ_NORM_RMS, 1e-5)
+    nq1, ne1 = sq.norm_quantize_act_mx(tail, torch.ones(K, device="cuda"), None, sq.SQ_NORM_RMS, 1e-5)
+    assert torch.equal(nq[-64:], nq1) and torch.equal(ne[-64:], ne1)
+    del x, y, nq, ne
+    w = sq.smooth_weights_mxfp4(torch.randn(8200, K, device="cuda", dtype=torch.bfloat16))
+    finite = torch.where((e == 255).any(dim=1, keepdim=True), torch.zeros_like(e), e)
+    log(f"gemm_mxfp4 M={M} N=8200 K={K}")
+    for tile in range(4):   # (a tile adds in one order, wherever its rows are)
+        y = sq.gemm_mxfp4(q, finite, *w, sq.SQ_MX_E4M3, out_dtype=torch.bfloat16, tile=tile)  # 4.4 GB
+        want = sq.gemm_mxfp4(q[-64:].contiguous(), finite[-64:].contiguous(), *w, sq.SQ_MX_E4M3,
+                             out_dtype=torch.bfloat16, tile=tile)
+        assert torch.equal(y[-64:].view(torch.int16), want.view(torch.int16))
+        assert not y[:-64].any()
 
 
 def test_explicit_stream(torch):

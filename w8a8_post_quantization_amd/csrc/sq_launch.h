@@ -98,9 +98,9 @@ void launch_dequant_mx(const uint8_t *q, const uint8_t *scale, int fmt, int64_t 
 void launch_norm_quant_mx(const void *x, int dt, int64_t M, int64_t K, int norm,
                           const float *gamma, const float *beta, float eps, int fmt, uint8_t *q,
                           uint8_t *scale, hipStream_t stream);
-void launch_gemm_mx(const uint8_t *xq, const uint8_t *xs, int x_fmt, const uint8_t *wq,
+bool launch_gemm_mx(const uint8_t *xq, const uint8_t *xs, int x_fmt, const uint8_t *wq,
                     const uint8_t *ws, int64_t M, int64_t N, int64_t K, void *y, int y_dt,
-                    hipStream_t stream, int force_tile = -1);
+                    hipStream_t stream, int force_tile = -1);  // false: no grid holds the tiles
 
 // Tiny device-to-device copies done by a kernel (no copy-engine or memset
 // nodes, so the calls stay capturable in a HIP graph).

@@ -94,7 +94,8 @@ int sq_gemm_mxfp4_tile(const uint8_t *xq, const uint8_t *x_scale, int x_fmt, con
     if (tile < -1 || tile > 3) return SQ_ERR_ARG;
     if (!valid_dt(y_dt)) return SQ_ERR_DTYPE;
     if (!valid_fmt(x_fmt)) return SQ_ERR_ARG;
-    if (bad_rows(M, K) || N < 0 || N > kMaxDim) return SQ_ERR_SHAPE;
+    // (rows and outputs of a last tile past the edge are counted in 32 bits)
+    if (bad_rows(M, K) || N < 0 || M > kMaxDim - 1023 || N > kMaxDim - 1023) return SQ_ERR_SHAPE;
     if (M == 0 || N == 0) return SQ_OK;
     if (K == 0) return SQ_ERR_SHAPE;  // an empty inner dimension
     if (K > 1 << 20) return SQ_ERR_UNSUPPORTED;  // 32-bit offsets inside a tile of 256 rows
@@ -102,7 +103,8 @@ int sq_gemm_mxfp4_tile(const uint8_t *xq, const uint8_t *x_scale, int x_fmt, con
     if (!aligned(xq, 16) || !aligned(wq, 16) || !aligned(x_scale, 4) || !aligned(w_scale, 4) ||
         !aligned(y, esize(y_dt)))
         return SQ_ERR_ALIGN;
-    sq::launch_gemm_mx(xq, x_scale, x_fmt, wq, w_scale, M, N, K, y, y_dt, st(stream), tile);
+    if (!sq::launch_gemm_mx(xq, x_scale, x_fmt, wq, w_scale, M, N, K, y, y_dt, st(stream), tile))
+        return SQ_ERR_UNSUPPORTED;
     return finish();
 }
 
