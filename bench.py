@@ -119,6 +119,7 @@ TRAFFIC_FILES = {"a3_smooth_weights": "a3_smooth_weights_prefill_30b_traffic.md"
 KERNEL_SOURCES = {"a3_smooth_weights": ["w8a8_post_quantization_amd/csrc/quant.hip",
                                         "w8a8_post_quantization_amd/csrc/sq_device.h"],
                   "a5_gemm": ["w8a8_post_quantization_amd/csrc/gemm.hip",
+                              "w8a8_post_quantization_amd/csrc/pipe_device.h",
                               "w8a8_post_quantization_amd/csrc/sq_device.h"]}
 
 

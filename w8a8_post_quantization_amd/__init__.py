@@ -546,9 +546,13 @@ def _vector(t, name, n):
 
 def _mx_rows(x, name):
     _torch()
-    x2 = x if x.dim() == 2 else x.reshape(-1, x.shape[-1])
-    _mx_check(x2, name, _dt_codes, 2)
-    return x2
+    if x.dim() != 2:
+        # (a view, never a copy: that would run on the current stream, the call
+        # perhaps on another)
+        _check(x, name, _dt_codes)
+        x = x.reshape(-1, x.shape[-1])
+    _mx_check(x, name, _dt_codes, 2)
+    return x
 
 
 def quantize_act_mx(x, inv_s=None, fmt=SQ_MX_E2M1, out=None, stream=None):
