@@ -1,5 +1,7 @@
 /*
  * sq.h - C ABI of the MI355X (gfx950) W8A8 SmoothQuant linear-layer library.
+ * The microscaled (MX) 4- and 8-bit forms of the quantizers and the product
+ * are in sq_mx.h.
  *
  * The library implements, as hand-written HIP kernels, the per-layer path of
  * SmoothQuant W8A8 post-training quantization and LLM.int8()'s mixed

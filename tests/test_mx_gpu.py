@@ -615,6 +615,21 @@ def test_layer_error_against_the_unquantized_product(torch):
     assert err["e4m3"] < 0.25 and err["e2m1"] < 0.5
 
 
+def test_rows_are_never_copied(torch):
+    """Inputs of more dimensions are viewed as rows; where that would take a copy
+    (on the current stream, whatever the call's own) the call is refused."""
+    g = torch.ones(64, device="cuda")
+    x = torch.randn(4, 6, 64, device="cuda")
+    q, e = sq.quantize_act_mx(x)
+    q1, e1 = sq.quantize_act_mx(x.reshape(24, 64))
+    assert torch.equal(q, q1) and torch.equal(e, e1)
+    for bad in (x[:, ::2], x.transpose(0, 1), x[..., :32]):
+        with pytest.raises(ValueError, match="contiguous"):
+            sq.quantize_act_mx(bad)
+        with pytest.raises(ValueError, match="contiguous"):
+            sq.norm_quantize_act_mx(bad, g)
+
+
 def test_empty_calls(torch):
     z = lambda *s: torch.empty(s, dtype=torch.uint8, device="cuda")  # noqa: E731
     x = torch.empty((0, 64), dtype=torch.float16, device="cuda")
