@@ -484,21 +484,22 @@ def _mx_call(name, tensors, args, stream, *last):
     for t in tensors:
         if t is not None and t.get_device() != dev:
             raise ValueError(f"operands on {tensors[0].device} and {t.device}")
-    cuda = _torch_mod.cuda
-    if cuda.current_device() == dev:
+    if _torch_mod.cuda.current_device() == dev:
         if stream is None and _raw_stream is not None:
             status = fn(*args, _raw_stream(dev), *last)
         else:
             status = fn(*args, _stream(stream), *last)
     else:
-        with cuda.device(dev):
+        with _torch_mod.cuda.device(dev):
             status = fn(*args, _stream(stream), *last)
     if status != 0:
         raise SQError(name, status)
 
 
+# The checks of these latency-bound calls are one expression each; the
+# functions that name what is wrong run only where it fails.
+
 def _mx_check(t, name, dtypes, ndim):
-    """_check's conditions in one expression (these calls are latency-bound)."""
     if not (t.is_cuda and t.dtype in dtypes and t.dim() == ndim and t.is_contiguous()):
         _check(t, name, dtypes, ndim)
 
@@ -512,35 +513,57 @@ def _mx_codes(fmt, K):
 
 def _mx_shapes(q, scale, fmt, name):
     """(rows, K) of codes [rows, K / 2] or [rows, K] and scales [rows, K / 32]."""
-    u8 = (_torch().uint8,)
-    _mx_check(q, name, u8, 2)
-    _mx_check(scale, "the scales of codes", u8, 2)
-    (rows, codes), (srows, blocks) = q.shape, scale.shape
-    if codes != _mx_codes(fmt, blocks * 32) or srows != rows:
+    u8 = _torch().uint8
+    if not (q.is_cuda and q.dtype == u8 and q.is_contiguous() and scale.is_cuda
+            and scale.dtype == u8 and scale.is_contiguous() and q.dim() == 2 == scale.dim()):
+        _check(q, name, (u8,), 2)
+        _check(scale, "the scales of codes", (u8,), 2)
+    rows, codes = q.shape
+    srows, blocks = scale.shape
+    K = blocks * 32
+    if codes != _mx_codes(fmt, K) or srows != rows:
         raise ValueError(f"{name} {tuple(q.shape)} and its scales {tuple(scale.shape)} disagree")
-    return rows, blocks * 32
+    return rows, K
+
+
+def _mx_empty(rows, cols, dtype, device):
+    # (0.3 us less than empty, which works the strides out)
+    return _torch_mod.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device)
 
 
 def _mx_out(out, rows, K, fmt, device):
     if K % 32:
         raise ValueError(f"rows of {K} elements: a multiple of 32 is needed")
     if out is None:
-        empty, u8 = _torch_mod.empty, _torch_mod.uint8
-        return (empty((rows, _mx_codes(fmt, K)), dtype=u8, device=device),
-                empty((rows, K // 32), dtype=u8, device=device))
+        u8 = _torch_mod.uint8
+        return (_mx_empty(rows, _mx_codes(fmt, K), u8, device),
+                _mx_empty(rows, K // 32, u8, device))
     q, scale = out
     if _mx_shapes(q, scale, fmt, "out") != (rows, K):
         raise ValueError(f"out {tuple(q.shape)} does not fit {rows} rows of {K} elements")
     return q, scale
 
 
+def _mx_result(out, rows, cols, dtype, device):
+    """The values' tensor: `out`, checked, or a new one."""
+    if out is None:
+        if dtype not in _dt_codes:
+            raise ValueError(f"out_dtype {dtype} not in {tuple(_dt_codes)}")
+        return _mx_empty(rows, cols, dtype, device)
+    _mx_check(out, "out", _dt_codes, 2)
+    if out.shape != (rows, cols):
+        raise ValueError(f"out {tuple(out.shape)} is not {(rows, cols)}")
+    return out
+
+
 def _vector(t, name, n):
     """The pointer of an fp32 vector of n elements, or None."""
     if t is None:
         return None
-    _mx_check(t, name, (_torch_mod.float32,), 1)
-    if t.shape[0] != n:
-        raise ValueError(f"{name} has {t.shape[0]} elements, not {n}")
+    if not (t.is_cuda and t.dtype == _torch_mod.float32 and t.dim() == 1 and t.is_contiguous()):
+        _check(t, name, (_torch_mod.float32,), 1)
+    if t.numel() != n:
+        raise ValueError(f"{name} has {t.numel()} elements, not {n}")
     return t.data_ptr()
 
 
@@ -551,7 +574,8 @@ def _mx_rows(x, name):
         # perhaps on another)
         _check(x, name, _dt_codes)
         x = x.reshape(-1, x.shape[-1])
-    _mx_check(x, name, _dt_codes, 2)
+    if not (x.is_cuda and x.dtype in _dt_codes and x.is_contiguous()):
+        _check(x, name, _dt_codes, 2)
     return x
 
 
@@ -598,13 +622,8 @@ def norm_quantize_act_mx(x, gamma, beta=None, norm=SQ_NORM_LAYER, eps=1e-5, fmt=
 def dequantize_mx(q, scale, fmt=SQ_MX_E2M1, out_dtype=None, out=None, stream=None):
     """The values [rows, K] (fp32 unless out_dtype says otherwise) that MX
     codes and scales stand for."""
-    torch = _torch()
     rows, K = _mx_shapes(q, scale, fmt, "q")
-    y = out if out is not None else torch.empty((rows, K), dtype=out_dtype or torch.float32,
-                                                device=q.device)
-    _mx_check(y, "out", _dt_codes, 2)
-    if tuple(y.shape) != (rows, K):
-        raise ValueError(f"out {tuple(y.shape)} is not {(rows, K)}")
+    y = _mx_result(out, rows, K, out_dtype or _torch_mod.float32, q.device)
     _mx_call("sq_dequantize_mx", (q, scale, y),
              (q.data_ptr(), scale.data_ptr(), fmt, rows, K, y.data_ptr(), _dt_codes[y.dtype]), stream)
     return y
@@ -615,16 +634,11 @@ def gemm_mxfp4(xq, x_scale, wq, w_scale, x_fmt=SQ_MX_E2M1, out_dtype=None, out=N
     """a5 in MX: y [M, N] (fp16 unless out_dtype says otherwise), the product
     of e2m1 weights with activations of x_fmt, summed in fp32.  tile (tests
     only) forces the block shape (include/sq_mx_test.h)."""
-    torch = _torch()
     M, K = _mx_shapes(xq, x_scale, x_fmt, "xq")
     N, Kw = _mx_shapes(wq, w_scale, SQ_MX_E2M1, "wq")
     if K != Kw:
         raise ValueError(f"K mismatch: xq has {K}, wq {Kw}")
-    y = out if out is not None else torch.empty((M, N), dtype=out_dtype or torch.float16,
-                                                device=xq.device)
-    _mx_check(y, "out", _dt_codes, 2)
-    if tuple(y.shape) != (M, N):
-        raise ValueError(f"out {tuple(y.shape)} is not {(M, N)}")
+    y = _mx_result(out, M, N, out_dtype or _torch_mod.float16, xq.device)
     args = (xq.data_ptr(), x_scale.data_ptr(), x_fmt, wq.data_ptr(), w_scale.data_ptr(), M, N, K,
             y.data_ptr(), _dt_codes[y.dtype])
     if tile is None:
