@@ -141,6 +141,21 @@ def test_quantize_every_scale(torch):
         assert_bits_equal(host(q, torch), q_o, "codes")
 
 
+@pytest.mark.parametrize("fmt", ["e2m1", "e4m3"])
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_quantize_every_16_bit_value(torch, dt, fmt):
+    """All 65536 bit patterns: signed zeros, subnormals, infinities, NaNs."""
+    bits = np.arange(1 << 16, dtype=np.uint16).reshape(-1, 32)
+    tdt = {"f16": torch.float16, "bf16": torch.bfloat16}[dt]
+    x = torch.from_numpy(bits.view(np.int16)).cuda().view(tdt)
+    f32 = bits.view(np.float16).astype(np.float32) if dt == "f16" else \
+        (bits.astype(np.uint32) << 16).view(np.float32)
+    q, e = sq.quantize_act_mx(x, None, FMT[fmt])
+    q_o, e_o = ref.quantize(f32, FMT[fmt])
+    assert_bits_equal(host(e, torch), e_o, "scales")
+    assert_bits_equal(host(q, torch), q_o, "codes")
+
+
 def test_rows_of_three_dimensions_and_out(torch):
     x = dev(_acts(5, 24, 96, "f16"), torch)
     q, e = sq.quantize_act_mx(x)

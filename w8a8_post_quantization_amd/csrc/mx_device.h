@@ -24,8 +24,23 @@ __device__ __forceinline__ Raw8<DT> load8(const void *x, int64_t i8) {
     return r;
 }
 
+// The halves of a word of two fp16 as fp32, exactly: h * 1 + -0 (-0 stays -0).
+// The plain conversion issues slower (layer norm of 16384 x 7168: 71 us with it,
+// 68 so).
+__device__ __forceinline__ void widen_f16(uint32_t w, float &lo, float &hi) {
+    asm("v_fma_mix_f32 %0, %1, 1.0, neg(0) op_sel_hi:[1,0,0]" : "=v"(lo) : "v"(w));
+    asm("v_fma_mix_f32 %0, %1, 1.0, neg(0) op_sel:[1,0,0] op_sel_hi:[1,0,0]" : "=v"(hi) : "v"(w));
+}
+
 template <int DT>
 __device__ __forceinline__ void widen8(const Raw8<DT> &r, float (&out)[8]) {
+    if constexpr (DT == F16) {
+        widen_f16(r.v[0].x, out[0], out[1]);
+        widen_f16(r.v[0].y, out[2], out[3]);
+        widen_f16(r.v[0].z, out[4], out[5]);
+        widen_f16(r.v[0].w, out[6], out[7]);
+        return;
+    }
     widen16<DT>(r.v[0], out);
     if constexpr (DT == F32) widen16<DT>(r.v[1], out + 4);
 }

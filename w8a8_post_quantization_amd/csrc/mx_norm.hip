@@ -182,9 +182,11 @@ __global__ __launch_bounds__(64 * NW) void mx_norm_kernel(const void *__restrict
 // no barrier, gamma and beta in LDS (four floats of a group's first half, then
 // of its second, so that successive lanes read successive 16 bytes).  With a
 // beta the kernel above holds 64 parameters a thread and two blocks a CU;
-// 16384 x 7168 fp16, layer norm to e2m1: 77 us here, 85 there (RMS norm 63 and
-// 65; without a beta 66 and 65, RMS 61 and 57: these stay there).  The row is
-// held as loaded and widened again for the output.
+// 16384 x 7168 fp16, layer norm to e2m1: 68..74 us here, 85 there (RMS norm 60
+// and 65; without a beta 66 and 65, RMS 61 and 57: these stay there).  The row
+// is held widened (as loaded, and widened again for the output: 72..77 us), in
+// 256 registers a thread at two waves a SIMD; four waves in 128 spill (99 us).
+// Bound by the VALU's issue, 13 instructions an element.
 template <int DT, int FMT, int NORM, int ITS>
 __global__ __launch_bounds__(512) void mx_norm_wave_kernel(const void *__restrict__ x, int64_t M,
                                                            int64_t K,
@@ -210,19 +212,22 @@ __global__ __launch_bounds__(512) void mx_norm_wave_kernel(const void *__restric
             const int c = 64 * i + lane;  // (past the row: its last block again)
             raw[i] = load8<DT, true>(x, row * K8 + (c < K8 ? c : K8 - 4 + (lane & 3)));
         }
+        float v[ITS][8];
         double s1 = 0.0, s2 = 0.0;
 #pragma unroll
         for (int i = 0; i < ITS; ++i) {
+            widen8<DT>(raw[i], v[i]);
             if (64 * i + lane < K8) {
-                float v[8];
-                widen8<DT>(raw[i], v);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
-                    const double d = (double)v[k];
+                    const double d = (double)v[i][k];
                     if constexpr (NORM == 0) s1 += d;
                     s2 = __builtin_fma(d, d, s2);
                 }
             }
+            // (kept: the compiler would widen again for the output)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) asm volatile("" : "+v"(v[i][k]));
         }
         if constexpr (NORM == 0) s1 = of_lane63(wave_sum_to_last(s1));
         s2 = of_lane63(wave_sum_to_last(s2));
@@ -234,11 +239,9 @@ __global__ __launch_bounds__(512) void mx_norm_wave_kernel(const void *__restric
 #pragma unroll
                 for (int i = 0; i < ITS; ++i) {
                     if (64 * i + lane < K8) {
-                        float v[8];
-                        widen8<DT>(raw[i], v);
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
-                            const double d = (double)v[k] - mean;
+                            const double d = (double)v[i][k] - mean;
                             c2 = __builtin_fma(d, d, c2);
                         }
                     }
@@ -254,19 +257,19 @@ __global__ __launch_bounds__(512) void mx_norm_wave_kernel(const void *__restric
             const int c = 64 * i + lane;
             const bool in = c < K8;
             const int cc = in ? c : K8 - 4 + (lane & 3);
-            float v[8], g[8], bt[8];
-            widen8<DT>(raw[i], v);
+            float g[8], bt[8];
             load_f32x8_planes(&sg[0][cc], &sg[1][cc], g);
             load_f32x8_planes(&sb[0][cc], &sb[1][cc], bt);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                if constexpr (NORM == 0) v[k] = v[k] - mu;
-                v[k] = v[k] * rstd;
-                v[k] = v[k] * g[k];
-                v[k] = v[k] + bt[k];
+                float y = v[i][k];
+                if constexpr (NORM == 0) y = y - mu;
+                y = y * rstd;
+                y = y * g[k];
+                v[i][k] = y + bt[k];
             }
             uint32_t e;
-            const MxCodes<FMT> cd = mx_encode8<FMT>(v, e);
+            const MxCodes<FMT> cd = mx_encode8<FMT>(v[i], e);
             if (in) mx_store8<FMT, true>(q, scale, row * K8 + c, cd, e);
         }
     }
