@@ -597,10 +597,10 @@ __global__ __launch_bounds__(512, 1) void mx_gemm_dec(MxArgs p) {
     };
     // Activations.  Up to 16 rows: each lane loads its own chunks (few lines
     // an instruction where rows repeat or are few).  More rows (XRING): such
-    // loads would look up 64 lines each (27.3 us against 26.0 at M = 32, N = 28672,
-    // K = 8192),
-    // so the rows come through the ring, XST stages before a pass's weights:
-    // 16 rows of a window's 64 SPW bytes, or of one of its halves (e4m3).
+    // loads would look up 64 lines each (27.3 us against 26.0 at M = 32,
+    // N = 28672, K = 8192), so the rows come through the ring, XST stages before
+    // a pass's weights: 16 rows of a window's 64 SPW bytes, or of one of its
+    // halves (e4m3).
     constexpr bool XRING = FT > 1;
     constexpr int XST = XRING ? FT * WPW * XH : 0;
     int ix = 0;  // activation stages of the pass issued
