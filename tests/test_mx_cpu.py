@@ -199,3 +199,24 @@ def test_binding_refuses_host_tensors():
                  lambda: sq.dequantize_mx(u, e), lambda: sq.gemm_mxfp4(u, e, u, e)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_binding_refuses_a_stream_of_another_gpu(monkeypatch):
+    """Refused before anything is asked of either GPU."""
+    torch = pytest.importorskip("torch")
+
+    class Operand:
+        device = torch.device("cuda", 0)
+
+        def get_device(self):
+            return 0
+
+    class Stream:
+        device = torch.device("cuda", 1)
+        cuda_stream = 0
+
+    calls = []
+    monkeypatch.setitem(sq._mx_fns, "sq_probe", lambda *a: calls.append(a) or 0)
+    with pytest.raises(ValueError, match="stream on cuda:1"):
+        sq._mx_call("sq_probe", (Operand(), None, Operand()), (), Stream())
+    assert not calls

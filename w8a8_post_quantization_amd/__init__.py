@@ -476,7 +476,8 @@ _mx_fns = {}
 def _mx_call(name, tensors, args, stream, *last):
     """Call `name` on the operands' own GPU.  `tensors` are all the operands
     (None allowed, the first present); `stream` (or that GPU's current stream)
-    gets the work; `last` are the arguments behind the stream."""
+    gets the work, and is one of that GPU (a kernel on another would read
+    memory that it cannot); `last` are the arguments behind the stream."""
     fn = _mx_fns.get(name)
     if fn is None:
         fn = _mx_fns[name] = getattr(lib(), name)
@@ -484,6 +485,8 @@ def _mx_call(name, tensors, args, stream, *last):
     for t in tensors:
         if t is not None and t.get_device() != dev:
             raise ValueError(f"operands on {tensors[0].device} and {t.device}")
+    if stream is not None and stream.device.index != dev:
+        raise ValueError(f"operands on {tensors[0].device}, stream on {stream.device}")
     if _torch_mod.cuda.current_device() == dev:
         if stream is None and _raw_stream is not None:
             status = fn(*args, _raw_stream(dev), *last)
