@@ -18,6 +18,8 @@ Names follow the C ABI:
   norm_quantize_act  fused fp16 norm -> int8 (per-token or per-tensor)
 Microscaled forms (``include/sq_mx.h``): quantize_act_mx,
 smooth_weights_mxfp4, norm_quantize_act_mx, dequantize_mx, gemm_mxfp4.
+Their ``stream=`` gets the work and owns the outputs that the call makes; the
+caller orders it behind the work that makes the operands.
 """
 from __future__ import annotations
 
@@ -529,30 +531,36 @@ def _mx_shapes(q, scale, fmt, name):
     return rows, K
 
 
-def _mx_empty(rows, cols, dtype, device):
+def _mx_empty(rows, cols, dtype, device, stream):
+    """A new output, allocated for the stream that writes it: memory of the
+    current stream's pool may be a freed tensor's, whose last kernels another
+    stream would not wait for."""
+    if stream is not None:
+        with _torch_mod.cuda.stream(stream):
+            return _mx_empty(rows, cols, dtype, device, None)
     # (0.3 us less than empty, which works the strides out)
     return _torch_mod.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device)
 
 
-def _mx_out(out, rows, K, fmt, device):
+def _mx_out(out, rows, K, fmt, device, stream):
     if K % 32:
         raise ValueError(f"rows of {K} elements: a multiple of 32 is needed")
     if out is None:
         u8 = _torch_mod.uint8
-        return (_mx_empty(rows, _mx_codes(fmt, K), u8, device),
-                _mx_empty(rows, K // 32, u8, device))
+        return (_mx_empty(rows, _mx_codes(fmt, K), u8, device, stream),
+                _mx_empty(rows, K // 32, u8, device, stream))
     q, scale = out
     if _mx_shapes(q, scale, fmt, "out") != (rows, K):
         raise ValueError(f"out {tuple(q.shape)} does not fit {rows} rows of {K} elements")
     return q, scale
 
 
-def _mx_result(out, rows, cols, dtype, device):
+def _mx_result(out, rows, cols, dtype, device, stream):
     """The values' tensor: `out`, checked, or a new one."""
     if out is None:
         if dtype not in _dt_codes:
             raise ValueError(f"out_dtype {dtype} not in {tuple(_dt_codes)}")
-        return _mx_empty(rows, cols, dtype, device)
+        return _mx_empty(rows, cols, dtype, device, stream)
     _mx_check(out, "out", _dt_codes, 2)
     if out.shape != (rows, cols):
         raise ValueError(f"out {tuple(out.shape)} is not {(rows, cols)}")
@@ -588,7 +596,7 @@ def quantize_act_mx(x, inv_s=None, fmt=SQ_MX_E2M1, out=None, stream=None):
     x2 = _mx_rows(x, "x")
     M, K = x2.shape
     inv = _vector(inv_s, "inv_s", K)
-    xq, xs = _mx_out(out, M, K, fmt, x2.device)
+    xq, xs = _mx_out(out, M, K, fmt, x2.device, stream)
     _mx_call("sq_quantize_act_mx", (x2, inv_s, xq, xs),
              (x2.data_ptr(), _dt_codes[x2.dtype], M, K, inv, fmt, xq.data_ptr(), xs.data_ptr()), stream)
     return xq, xs
@@ -601,7 +609,7 @@ def smooth_weights_mxfp4(w, s=None, row_mul=None, out=None, stream=None):
     _mx_check(w, "w", _dt_codes, 2)
     N, K = w.shape
     sp, rp = _vector(s, "s", K), _vector(row_mul, "row_mul", N)
-    wq, ws = _mx_out(out, N, K, SQ_MX_E2M1, w.device)
+    wq, ws = _mx_out(out, N, K, SQ_MX_E2M1, w.device, stream)
     _mx_call("sq_smooth_weights_mxfp4", (w, s, row_mul, wq, ws),
              (w.data_ptr(), _dt_codes[w.dtype], N, K, rp, sp, wq.data_ptr(), ws.data_ptr()), stream)
     return wq, ws
@@ -615,7 +623,7 @@ def norm_quantize_act_mx(x, gamma, beta=None, norm=SQ_NORM_LAYER, eps=1e-5, fmt=
     if gamma is None:
         raise ValueError("gamma is needed")
     g, b = _vector(gamma, "gamma", K), _vector(beta, "beta", K)
-    xq, xs = _mx_out(out, M, K, fmt, x2.device)
+    xq, xs = _mx_out(out, M, K, fmt, x2.device, stream)
     _mx_call("sq_norm_quantize_act_mx", (x2, gamma, beta, xq, xs),
              (x2.data_ptr(), _dt_codes[x2.dtype], M, K, norm, g, b, eps, fmt, xq.data_ptr(), xs.data_ptr()),
              stream)
@@ -626,7 +634,7 @@ def dequantize_mx(q, scale, fmt=SQ_MX_E2M1, out_dtype=None, out=None, stream=Non
     """The values [rows, K] (fp32 unless out_dtype says otherwise) that MX
     codes and scales stand for."""
     rows, K = _mx_shapes(q, scale, fmt, "q")
-    y = _mx_result(out, rows, K, out_dtype or _torch_mod.float32, q.device)
+    y = _mx_result(out, rows, K, out_dtype or _torch_mod.float32, q.device, stream)
     _mx_call("sq_dequantize_mx", (q, scale, y),
              (q.data_ptr(), scale.data_ptr(), fmt, rows, K, y.data_ptr(), _dt_codes[y.dtype]), stream)
     return y
@@ -641,7 +649,7 @@ def gemm_mxfp4(xq, x_scale, wq, w_scale, x_fmt=SQ_MX_E2M1, out_dtype=None, out=N
     N, Kw = _mx_shapes(wq, w_scale, SQ_MX_E2M1, "wq")
     if K != Kw:
         raise ValueError(f"K mismatch: xq has {K}, wq {Kw}")
-    y = _mx_result(out, M, N, out_dtype or _torch_mod.float16, xq.device)
+    y = _mx_result(out, M, N, out_dtype or _torch_mod.float16, xq.device, stream)
     args = (xq.data_ptr(), x_scale.data_ptr(), x_fmt, wq.data_ptr(), w_scale.data_ptr(), M, N, K,
             y.data_ptr(), _dt_codes[y.dtype])
     if tile is None:
