@@ -31,6 +31,14 @@ __device__ __forceinline__ double inv_sqrt(double v) {
     return y;
 }
 
+// sum / k, rounded: the product with 1 / k alone may be off by a last place, and
+// a row of one value v would then have a mean beside v (so at K = 1568, 5152 and
+// 33 more lengths) and a sigma^2 above 0.
+__device__ __forceinline__ double row_mean(double sum, double k, double inv_k) {
+    const double m = sum * inv_k;
+    return __builtin_fma(__builtin_fma(-m, k, sum), inv_k, m);
+}
+
 // (Newton's steps make NaN of the ends: a zero row with eps = 0 has an infinity
 // as defined, a row with an infinity under the RMS norm 0)
 __device__ __forceinline__ float row_rstd(double ve) {
@@ -131,7 +139,7 @@ __global__ __launch_bounds__(64 * NW) void mx_norm_kernel(const void *__restrict
         }
         total(s1, s2, par);
         par ^= 1;
-        const double mean = NORM == 0 ? s1 * inv_k : 0.0;
+        const double mean = NORM == 0 ? row_mean(s1, (double)K, inv_k) : 0.0;
         double var = s2 * inv_k - mean * mean;
         if constexpr (NORM == 0) {
             if (mean * mean > 256.0 * var) {  // (uniform over the row's waves)
@@ -231,7 +239,7 @@ __global__ __launch_bounds__(512) void mx_norm_wave_kernel(const void *__restric
         }
         if constexpr (NORM == 0) s1 = of_lane63(wave_sum_to_last(s1));
         s2 = of_lane63(wave_sum_to_last(s2));
-        const double mean = NORM == 0 ? s1 * inv_k : 0.0;
+        const double mean = NORM == 0 ? row_mean(s1, (double)K, inv_k) : 0.0;
         double var = s2 * inv_k - mean * mean;
         if constexpr (NORM == 0) {
             if (mean * mean > 256.0 * var) {
