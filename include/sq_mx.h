@@ -72,7 +72,10 @@ int sq_smooth_weights_mxfp4(const void *w, int dt, int64_t N, int64_t K, const f
  *   norm   SQ_NORM_LAYER: mu = mean_j x_j, sigma^2 = mean_j (x_j - mu)^2;
  *          SQ_NORM_RMS:   mu = 0,          sigma^2 = mean_j x_j^2
  *          summed in double; rstd = 1 / sqrt(sigma^2 + eps) in double; then mu
- *          and rstd rounded to fp32
+ *          and rstd rounded to fp32.  The order of the sums depends on M and K
+ *          (the same call gives the same bits every time): where a double
+ *          result lies at a rounding border, less than one row in 2^13, a
+ *          row's mu or rstd may differ in its last place with M.
  *   gamma  [K] fp32; beta [K] fp32 or NULL; eps >= 0, finite
  *   per element in fp32: n = fl(fl(x - mu) * rstd), y = fl(n * gamma_j), then
  *          y = fl(y + beta_j) if beta
@@ -85,8 +88,9 @@ int sq_norm_quantize_act_mx(const void *x, int dt, int64_t M, int64_t K, int nor
 
 /*
  * The values of codes and scales: y = value(code) * 2^(e - 127), narrowed to
- * y_dt with round-to-nearest-even (fp32 and bf16 hold every value the
- * quantizers produce; e = 255 gives NaN).
+ * y_dt with round-to-nearest-even (fp32 holds every value the quantizers
+ * produce, bf16 all but those of e4m3 blocks with e < 3, which reach below its
+ * smallest subnormal 2^-133; e = 255 gives NaN).
  *   q [rows, K / 2] or [rows, K], scale [rows, K / 32], y [rows, K] of y_dt
  * K % 32 == 0; K > 0 when rows > 0.
  */
