@@ -15,6 +15,7 @@
 #include <type_traits>
 
 #include "mx_device.h"
+#include "resident.h"
 #include "sq_launch.h"
 
 namespace sq {
@@ -285,24 +286,38 @@ __global__ __launch_bounds__(512) void mx_norm_wave_kernel(const void *__restric
     }
 }
 
+// As many blocks as the current GPU holds at once, so that all walk down the
+// rows together (a second, partial round of blocks would double the time where
+// the last round is short).
+template <auto Kernel>
+static int64_t resident_blocks(int threads) {
+    int gpu = -1;
+    if (hipGetDevice(&gpu) != hipSuccess) gpu = -1;
+    return once_per_gpu<Kernel>(gpu, [&]() -> int64_t {
+        int n = 0, cus = 0;
+        if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, Kernel, threads, 0) != hipSuccess || n < 1) n = 1;
+        if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, gpu) != hipSuccess || cus < 1)
+            cus = 256;
+        return (int64_t)n * cus;
+    });
+}
+
+template <int DT, int FMT, int NORM, bool HAS_BETA, int NW, int ITS, bool NT>
+static void launch_mn_nt(const void *x, int64_t M, int64_t K, const float *gamma, const float *beta,
+                         float eps, uint8_t *q, uint8_t *scale, hipStream_t stream) {
+    constexpr auto kernel = mx_norm_kernel<DT, FMT, NORM, HAS_BETA, NW, ITS, NT>;
+    const int64_t resident = resident_blocks<kernel>(64 * NW);
+    const dim3 grid((unsigned)(M < resident ? M : resident));
+    kernel<<<grid, 64 * NW, 0, stream>>>(x, M, K, gamma, beta, eps, q, scale);
+}
+
 template <int DT, int FMT, int NORM, bool HAS_BETA, int NW, int ITS>
 static void launch_mn_t(const void *x, int64_t M, int64_t K, const float *gamma, const float *beta,
                         float eps, uint8_t *q, uint8_t *scale, hipStream_t stream) {
-    auto launch = [&](auto kernel) {
-        // As many blocks as the chip holds at once, so that all walk down the
-        // rows together (a second, partial round of blocks would double the
-        // time where the last round is short).
-        static const int64_t resident = [&] {
-            int n = 0;
-            if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, 64 * NW, 0) != hipSuccess || n < 1)
-                n = 1;
-            return (int64_t)n * 256;
-        }();
-        const dim3 grid((unsigned)(M < resident ? M : resident));
-        kernel<<<grid, 64 * NW, 0, stream>>>(x, M, K, gamma, beta, eps, q, scale);
-    };
-    if (M * K * dt_bytes(DT) > kNtLoadBytes) launch(mx_norm_kernel<DT, FMT, NORM, HAS_BETA, NW, ITS, true>);
-    else launch(mx_norm_kernel<DT, FMT, NORM, HAS_BETA, NW, ITS, false>);
+    if (M * K * dt_bytes(DT) > kNtLoadBytes)
+        launch_mn_nt<DT, FMT, NORM, HAS_BETA, NW, ITS, true>(x, M, K, gamma, beta, eps, q, scale, stream);
+    else
+        launch_mn_nt<DT, FMT, NORM, HAS_BETA, NW, ITS, false>(x, M, K, gamma, beta, eps, q, scale, stream);
 }
 
 template <int DT, int FMT, int NORM, bool HAS_BETA>
