@@ -115,7 +115,8 @@ int sq_dequantize_mx(const uint8_t *q, const uint8_t *scale, int fmt, int64_t ro
  * up to four pieces, each cut to the sum's last place.
  * K % 32 == 0, 32 <= K <= 1048576 when M, N > 0 (SQ_ERR_UNSUPPORTED above);
  * M, N <= 2^31 - 1024, in fewer tiles than 2^23 (SQ_ERR_UNSUPPORTED; a tile
- * is 64 x 128 outputs at the least, 32 x 16 for K < 256).
+ * is 64 x 128 outputs at the least; for K < 256 32 x 32, N <= 16 32 x 16, and
+ * fewer than 2^25 of them).
  */
 int sq_gemm_mxfp4(const uint8_t *xq, const uint8_t *x_scale, int x_fmt, const uint8_t *wq,
                   const uint8_t *w_scale, int64_t M, int64_t N, int64_t K, void *y, int y_dt,

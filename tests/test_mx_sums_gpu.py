@@ -101,3 +101,23 @@ def test_sums_over_scales_that_differ(torch, M, N, K, spread, fmt):
     worst = float((np.abs(y - exact) / tol).max())
     print(f"\ngemm_mxfp4 {fmt} M={M} N={N} K={K} spread={spread}: worst error / bound {worst:.3f}")
     assert worst <= 1
+
+
+@pytest.mark.parametrize("fmt", ["e2m1", "e4m3"])
+@pytest.mark.parametrize("M,N,K", [(33, 17, 32), (40, 512, 160), (1000, 1100, 64), (1030, 1000, 224), (4099, 300, 128),
+                                   (70000, 16, 96), (65, 16500, 192), (2, 40, 224), (16, 33000, 128), (1, 17000, 160),
+                                   (31, 17010, 32), (20, 3, 224)])
+def test_short_inner_lengths(torch, M, N, K, fmt):
+    """K < 256 with many rows: one and two windows, one and two groups of weight
+    rows a block, ragged slabs.  All scales 1: e2m1 terms are multiples of 0.25
+    and their sums below 36 * 224, so exact in any order, as the e4m3 ones."""
+    if fmt == "e4m3":
+        _exact(torch, M, N, K, None)
+        return
+    rng = np.random.default_rng(M + N + K)
+    xq, wq = (rng.integers(0, 256, (r, K // 2), dtype=np.uint8) for r in (M, N))
+    xs, ws = (np.full((r, K // 32), 127, np.uint8) for r in (M, N))
+    want = ref.decode(xq, xs, ref.E2M1) @ ref.decode(wq, ws, ref.E2M1).T
+    log(f"gemm_mxfp4 exact sums M={M} N={N} K={K} e2m1")
+    y = host(sq.gemm_mxfp4(*[dev(a, torch) for a in (xq, xs, wq, ws)], out_dtype=torch.float32), torch)
+    assert np.array_equal(y, want)

@@ -12,7 +12,8 @@
 // Weight rows are the instruction's first operand (rows of its result).
 //
 // Two kernels:
-//  * mx_gemm_dec  M <= 32 (decode), bound by the weight stream; also K < 256.
+//  * mx_gemm_dec  M <= 32 (decode), bound by the weight stream; also K < 256,
+//                 bound by the outputs' stores.
 //  * mx_gemm_pp   M > 32: both operands through LDS rings filled by
 //                 direct-to-LDS loads.
 #include <type_traits>
@@ -507,15 +508,16 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx_gemm_pp(MxArgs p) {
 // ---------------------------------------------------------------- decode
 
 // M <= 32, or K < 256 in slabs of 32 tokens (tiles_n blocks a slab).  Bound by
-// the weight stream, so a block of eight waves reads each byte of its weight
-// rows once and everything else is kept small: the waves split K, each holds
-// its part of the 16 FT activation rows for all of the block's weight rows,
-// and streams its part of these, a group of 16 rows at a time, through a
-// private ring of S LDS stages by direct-to-LDS loads.  No barrier until the
-// end, where the waves' sums are added through LDS in wave order.
+// the weight stream, so a block of NW waves (eight, for K < 256 as many as it has
+// windows) reads each byte of its weight rows once and everything else is kept
+// small: the waves split K, each holds its part of the 16 FT activation rows for
+// all of the block's weight rows, and streams its part of these, a group of 16
+// rows at a time, through a private ring of S LDS stages by direct-to-LDS loads.
+// No barrier until the end, where the waves' sums are added through LDS in wave
+// order.
 //
 // A stage is a window of 128 SPW elements (64 SPW bytes) of a group's rows.
-// Wave w has windows w, w + 8, ..., and holds the activations of WPW of them at
+// Wave w has windows w, w + NW, ..., and holds the activations of WPW of them at
 // a time: the eight waves read successive bytes of a row together (with two
 // neighbouring windows a wave instead, the waves in step read every other
 // 256 bytes: 27 us against 23 at M = 1, N = 28672, K = 8192).  Which blocks of a
@@ -561,21 +563,21 @@ __device__ __forceinline__ int join_slot(int ri, int rg, int group) {
     return 16 * rg + (ri ^ ((4 * rg + group) & 15));
 }
 
-// The sums of the eight waves in wave order, four successive outputs a thread.
-template <int YDT, int FT, int NG>
+// The sums of the NW waves in wave order, four successive outputs a thread.
+template <int YDT, int FT, int NG, int NW>
 __device__ __forceinline__ void dec_store(const MxArgs &p, const f32x4 *red, int64_t ms, int M,
                                           int n0) {
     using T = typename OutT<YDT>::T;
     const int N = p.N, quads = p.groups * 4;
     const bool vec_y = N % 4 == 0 && ((uintptr_t)p.y % (4 * sizeof(T))) == 0;
-    for (int e = threadIdx.x; e < quads * M; e += 512) {
+    for (int e = threadIdx.x; e < quads * M; e += 64 * NW) {
         const int nq = e % quads, m = e / quads;
         const int g = nq >> 2, n = n0 + nq * 4;
         if (n >= N) continue;
         const f32x4 *r = red + (g * FT + (m >> 4)) * 64 + join_slot(m & 15, nq & 3, g);
         f32x4 s = r[0];
 #pragma unroll
-        for (int w = 1; w < 8; ++w) s += r[w * (NG * FT * 64)];
+        for (int w = 1; w < NW; ++w) s += r[w * (NG * FT * 64)];
         T h[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) h[k] = narrow<YDT>(s[k]);
@@ -591,9 +593,9 @@ __device__ __forceinline__ void dec_store(const MxArgs &p, const f32x4 *red, int
     }
 }
 
-template <int XF, int FT, int SPW, int WPW, int NG, int S>
-__global__ __launch_bounds__(512, 1) void mx_gemm_dec(MxArgs p) {
-    constexpr int NW = 8, XH = XF == E4M3 ? 2 : 1;
+template <int XF, int FT, int SPW, int WPW, int NG, int S, int NW>
+__global__ __launch_bounds__(64 * NW, 1) void mx_gemm_dec(MxArgs p) {
+    constexpr int XH = XF == E4M3 ? 2 : 1;
     constexpr int SLOT = SPW * 1024;          // one stage: 16 rows of 64 SPW bytes
     constexpr int RING = S * SLOT;
     constexpr int RED = NG * FT * 1024;       // one wave's sums
@@ -818,9 +820,9 @@ __global__ __launch_bounds__(512, 1) void mx_gemm_dec(MxArgs p) {
                 red[((wave * NG + i) * FT + f) * 64 + join_slot(ri, rg, i)] = acc[i][f];
         }
     __syncthreads();
-    if (p.y_dt == F32) dec_store<F32, FT, NG>(p, red, ms, M, n0);
-    else if (p.y_dt == F16) dec_store<F16, FT, NG>(p, red, ms, M, n0);
-    else dec_store<BF16, FT, NG>(p, red, ms, M, n0);
+    if (p.y_dt == F32) dec_store<F32, FT, NG, NW>(p, red, ms, M, n0);
+    else if (p.y_dt == F16) dec_store<F16, FT, NG, NW>(p, red, ms, M, n0);
+    else dec_store<BF16, FT, NG, NW>(p, red, ms, M, n0);
 }
 
 // ---------------------------------------------------------------- launch
@@ -839,15 +841,17 @@ static bool launch_pp(MxArgs &a, hipStream_t stream) {
     return true;
 }
 
-template <int XF, int FT, int SPW, int WPW, int NG, int S>
+template <int XF, int FT, int SPW, int WPW, int NG, int S, int NW = 8>
 static bool launch_dec_t(MxArgs &a, hipStream_t stream) {
     a.tiles_n = (a.N + 16 * a.groups - 1) / (16 * a.groups);
     const int64_t blocks = (((int64_t)a.M + 16 * FT - 1) / (16 * FT)) * a.tiles_n;
-    if (!grid_holds(blocks, 512)) return false;
-    mx_gemm_dec<XF, FT, SPW, WPW, NG, S><<<dim3((unsigned)blocks), 512, 0, stream>>>(a);
+    // (one limit for one wave a block and two, the one that sq_mx.h states)
+    if (!grid_holds(blocks, NW == 8 ? 512 : 128)) return false;
+    mx_gemm_dec<XF, FT, SPW, WPW, NG, S, NW><<<dim3((unsigned)blocks), 64 * NW, 0, stream>>>(a);
     return true;
 }
 
+// M <= 32, K >= 256.
 template <int XF, int FT>
 static bool launch_dec(MxArgs &a, hipStream_t stream) {
     // groups of 16 weight rows per block: an equal share for the 256 CUs of
@@ -874,10 +878,34 @@ static bool launch_dec(MxArgs &a, hipStream_t stream) {
     }
 }
 
+// K < 256: slabs of 16 FT tokens, as many waves a block as K has windows of 128
+// elements (NW), and two groups of weight rows a block, one where that leaves
+// fewer than four blocks a CU.  us, fp16 outputs:
+//   groups            4096 x 4096 x 64   x 224   1693 x 11440 x 64   64 x 4096 x 128
+//   e2m1  1                31.4          43.6          42.7                3.3
+//         2                19.1          26.2          27.6                3.7
+//         4                26.4          44.9          34.5                6.1
+//         8                21.3          35.9          28.2                8.2
+//         launch_dec's     81.5          90.6         172.2                3.5
+//   e4m3  1                38.2          58.6          49.6                3.8
+//         2                23.3          34.8          32.9                4.1
+//         8                22.9          39.6          30.8                8.9
+// and of few tokens, launch_dec's against these: 8 x 70000 x 64 10.0 and 4.0,
+// 32 x 28672 x 224 8.2 and 5.1, 1 x 4096 x 64 2.7 and 2.5.  (fp32 outputs of
+// 4096 x 4096 x 64 20.5; filling them alone takes 12.)
+template <int XF, int FT, int NW>
+static bool launch_short(MxArgs &a, hipStream_t stream) {
+    const int64_t blocks = (((int64_t)a.M + 16 * FT - 1) / (16 * FT)) * (((int64_t)a.N + 15) / 16);
+    a.groups = blocks > 1024 && a.N > 16 ? 2 : 1;
+    return launch_dec_t<XF, FT, 1, 1, 2, 3, NW>(a, stream);
+}
+
 template <int XF>
 static bool launch_mx(MxArgs &a, hipStream_t stream, int tile) {
+    if (a.K <= 128) return a.M <= 16 ? launch_short<XF, 1, 1>(a, stream) : launch_short<XF, 2, 1>(a, stream);
+    if (a.K < 256) return a.M <= 16 ? launch_short<XF, 1, 2>(a, stream) : launch_short<XF, 2, 2>(a, stream);
     if (a.M <= 16) return launch_dec<XF, 1>(a, stream);
-    if (a.M <= 32 || a.K < 256) return launch_dec<XF, 2>(a, stream);
+    if (a.M <= 32) return launch_dec<XF, 2>(a, stream);
     if (a.K % 128 != 0) {
         if (tile == 3) return launch_pp<XF, 64, 128, 2, 4, 2, 0>(a, stream);
         // (e4m3: one m-fragment a wave, so that fewer waves split the same
