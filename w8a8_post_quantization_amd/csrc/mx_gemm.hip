@@ -936,10 +936,22 @@ static bool launch_mx(MxArgs &a, hipStream_t stream, int tile) {
 //         4096 x 1024 x 1024          10.9    8.5    7.2    7.4
 //         256 x 28672 x 7168          60.5   41.3   41.0   60.2
 //         64 x 28672 x 8192           58.0   39.8   40.9   30.6
-//   e4m3  4096 x 4096 x 1024          21.4     -    26.2   34.0
-//         2048 x 4096 x 4096          31.0     -    36.1   44.8
-//         256 x 28672 x 7168          61.5     -    61.5   80.0
-//         333 x 5001 x 1024           13.3     -     9.0    6.7
+//         256 x 4096 x 4096           25.6   17.5   16.1   11.1
+//         128 x 8192 x 8192           56.0   34.2   38.3   23.2
+//         33 x 1024 x 4096            23.6   16.3   15.5   10.5
+//         2048 x 512 x 4096           25.4   17.6   16.0   11.0
+//   e4m3  4096 x 14336 x 4096        317       -   389    543
+//         4096 x 4096 x 1024          29.8     -    35.9   50.4
+//         2048 x 4096 x 4096          49.3     -    59.4   80.3
+//         256 x 28672 x 7168          87.4     -    97.9  136
+//         256 x 4096 x 4096           39.7     -    26.0   20.3
+//         128 x 28672 x 8192          81.6     -    56.6   81.8
+//         33 x 1024 x 4096            37.5     -    24.5   19.1
+//         333 x 5001 x 1024           16.6     -    11.9    9.0
+// Over 54 shapes a format, M = 33 .. 8192 and N = 300 .. 28672, the choice was the
+// fastest shape or within 8 % of it but for e2m1 with 64 x 128 tiles in two short
+// rounds, which run two blocks a CU (1000 x 4096 x 4096 20.3 us, 17.6 in those;
+// 8192 x 300 x 1024 10.7, 8.2).
 static int mx_pick_tile(int x_fmt, int64_t M, int64_t N, int64_t K) {
     struct C { int bm, bn; double rate; };
     const C e2[4] = {{256, 256, 1.0}, {256, 128, 0.85}, {128, 128, 0.7}, {64, 128, 0.5}};

@@ -193,8 +193,8 @@ __global__ __launch_bounds__(64 * NW) void mx_norm_kernel(const void *__restrict
 // no barrier, gamma and beta in LDS (four floats of a group's first half, then
 // of its second, so that successive lanes read successive 16 bytes).  With a
 // beta the kernel above holds 64 parameters a thread and two blocks a CU;
-// 16384 x 7168 fp16, layer norm to e2m1: 68..74 us here, 85 there (RMS norm 60
-// and 65; without a beta 66 and 65, RMS 61 and 57: these stay there).  The row
+// 16384 x 7168 fp16, layer norm to e2m1: 66..74 us here, 77 there (RMS norm 61
+// and 66; without a beta 66 and 65, RMS 61 and 57: these stay there).  The row
 // is held widened (as loaded, and widened again for the output: 72..77 us), in
 // 256 registers a thread at two waves a SIMD; four waves in 128 spill (99 us).
 // Bound by the VALU's issue, 13 instructions an element.
@@ -339,7 +339,12 @@ static void launch_mn(const void *x, int64_t M, int64_t K, const float *gamma, c
         else if (K <= 8192) go(c8, c2);
         else go(c8, c4);
     } else if (DT != F32 && HAS_BETA && M >= 4096 && K > 4096 && K <= 8192) {
-        // (256 blocks of 8 rows: at least two rows a wave)
+        // (256 blocks of 8 rows: at least two rows a wave.  us so and in the
+        // kernel below, layer norm of fp16 to e2m1: 4097 x 7168 21.3 and 24.3,
+        // 5120 28.4 and 28.5, 6145 29.9 and 32.8, 16384 66 and 77; 4097 x 4128
+        // 14.8 and 20.0, 6000 x 5120 23.1 and 29.3, 8192 x 8192 41.7 and 43.0;
+        // RMS norms the same or up to 3 % slower so at 8192 columns; 1024 x 7168
+        // 10.4 and 9.2)
         if constexpr (DT != F32 && HAS_BETA)
             mx_norm_wave_kernel<DT, FMT, NORM, 16>
                 <<<256, 512, 0, stream>>>(x, M, K, gamma, beta, eps, q, scale);
