@@ -106,8 +106,8 @@ template <int NL, bool NT>
 __device__ __forceinline__ void lds_dma_group(const int8_t *const *g, uint32_t lds_base) {
     static_assert(NL >= 1 && NL <= 4, "one M0 covers 4 KB of instruction offsets");
     const int8_t *b0 = g[0];
-    const int8_t *b1 = NL > 1 ? g[1] - 1024 : nullptr;
-    const int8_t *b2 = NL > 2 ? g[2] - 2048 : nullptr;
+    const int8_t *b1 = NL > 1 ? g[1] - 1 * 1024 : nullptr;
+    const int8_t *b2 = NL > 2 ? g[2] - 2 * 1024 : nullptr;
     const int8_t *b3 = NL > 3 ? g[3] - 3 * 1024 : nullptr;
 #define SQ_DMA_ASM(HINT)                                                                   \
     if constexpr (NL == 1) {                                                               \
@@ -117,19 +117,19 @@ __device__ __forceinline__ void lds_dma_group(const int8_t *const *g, uint32_t l
     } else if constexpr (NL == 2) {                                                        \
         asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\t"                                    \
                      "global_load_lds_dwordx4 %0, off" HINT "\n\t"                        \
-                     "global_load_lds_dwordx4 %1, off offset:1024" HINT                    \
+                     "global_load_lds_dwordx4 %1, off offset:0x400" HINT                    \
                      : : "v"(b0), "v"(b1), "s"(lds_base) : "memory", "m0");                \
     } else if constexpr (NL == 3) {                                                        \
         asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\t"                                    \
                      "global_load_lds_dwordx4 %0, off" HINT "\n\t"                        \
-                     "global_load_lds_dwordx4 %1, off offset:1024" HINT "\n\t"            \
-                     "global_load_lds_dwordx4 %2, off offset:2048" HINT                    \
+                     "global_load_lds_dwordx4 %1, off offset:0x400" HINT "\n\t"            \
+                     "global_load_lds_dwordx4 %2, off offset:0x800" HINT                    \
                      : : "v"(b0), "v"(b1), "v"(b2), "s"(lds_base) : "memory", "m0");       \
     } else {                                                                               \
         asm volatile("s_mov_b32 m0, %4\n\ts_nop 0\n\t"                                    \
                      "global_load_lds_dwordx4 %0, off" HINT "\n\t"                        \
-                     "global_load_lds_dwordx4 %1, off offset:1024" HINT "\n\t"            \
-                     "global_load_lds_dwordx4 %2, off offset:2048" HINT "\n\t"            \
+                     "global_load_lds_dwordx4 %1, off offset:0x400" HINT "\n\t"            \
+                     "global_load_lds_dwordx4 %2, off offset:0x800" HINT "\n\t"            \
                      "global_load_lds_dwordx4 %3, off offset:0xc00" HINT                    \
                      : : "v"(b0), "v"(b1), "v"(b2), "v"(b3), "s"(lds_base)                  \
                      : "memory", "m0");                                                    \
@@ -197,11 +197,11 @@ __device__ __forceinline__ void lds_dma_based(const uint32_t *off, const void *b
     for (int j0 = 0; j0 < N; j0 += 4) {
         if constexpr (B == 4) {
             static_assert(!NT, "no nontemporal form");
-            SQ_DMA_BASED("global_load_lds_dword", "", "256", "512", "768")
+            SQ_DMA_BASED("global_load_lds_dword", "", "0x100", "0x200", "0x300")
         } else if constexpr (NT) {
-            SQ_DMA_BASED("global_load_lds_dwordx4", " nt", "1024", "2048", "0xc00")
+            SQ_DMA_BASED("global_load_lds_dwordx4", " nt", "0x400", "0x800", "0xc00")
         } else {
-            SQ_DMA_BASED("global_load_lds_dwordx4", "", "1024", "2048", "0xc00")
+            SQ_DMA_BASED("global_load_lds_dwordx4", "", "0x400", "0x800", "0xc00")
         }
     }
 #undef SQ_DMA_BASED
