@@ -17,13 +17,16 @@ Names follow the C ABI:
   fold_norm          1/s folded into the preceding norm's gamma / beta
   norm_quantize_act  fused fp16 norm -> int8 (per-token or per-tensor)
 Microscaled forms (``include/sq_mx.h``): quantize_act_mx,
-smooth_weights_mxfp4, norm_quantize_act_mx, dequantize_mx, gemm_mxfp4.
+smooth_weights_mxfp4, norm_quantize_act_mx, dequantize_mx, gemm_mxfp4; a
+microscaled cache of keys and values (``include/sq_kv.h``): new_kv_cache_mx,
+rope_frequencies, rope_quantize_kv_mx, dequantize_kv_mx, attention_kv_mx.
 Their ``stream=`` gets the work and owns the outputs that the call makes; the
 caller orders it behind the work that makes the operands.
 """
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import re
 
@@ -33,11 +36,13 @@ HEADER = os.path.join(os.path.dirname(HERE), "include", "sq.h")
 MX_HEADER = os.path.join(os.path.dirname(HERE), "include", "sq_mx.h")
 MX_TEST_HEADER = os.path.join(os.path.dirname(HERE), "include", "sq_mx_test.h")
 TEST_HEADER = os.path.join(os.path.dirname(HERE), "include", "sq_test.h")
+KV_HEADER = os.path.join(os.path.dirname(HERE), "include", "sq_kv.h")
 
 SQ_F32, SQ_F16, SQ_BF16 = 0, 1, 2
 SQ_PER_TENSOR_STATIC, SQ_PER_TOKEN_DYNAMIC = 0, 1
 SQ_NORM_LAYER, SQ_NORM_RMS = 0, 1
 SQ_MX_E2M1, SQ_MX_E4M3 = 0, 1
+SQ_ROPE_HALF, SQ_ROPE_INTERLEAVED = 0, 1
 
 _lib = None
 
@@ -45,6 +50,16 @@ _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I = ctypes.c_int
 _F = ctypes.c_float
+
+
+class _KvCache(ctypes.Structure):
+    """sq_kv_cache of include/sq_kv.h."""
+    _fields_ = [("kq", _P), ("ks", _P), ("vq", _P), ("vs", _P), ("pages", _I64), ("heads", _I64),
+                ("page", _I64), ("dim", _I64), ("fmt", _I)]
+
+
+_STRIDES = _I64 * 2
+_CACHE_P, _STRIDE_P = ctypes.POINTER(_KvCache), ctypes.POINTER(_I64)
 
 SIGNATURES = {
     "sq_status_str": (ctypes.c_char_p, [_I]),
@@ -74,6 +89,13 @@ SIGNATURES = {
     "sq_norm_quantize_act_mx": (_I, [_P, _I, _I64, _I64, _I, _P, _P, _F, _I, _P, _P, _P]),
     "sq_dequantize_mx": (_I, [_P, _P, _I, _I64, _I64, _P, _I, _P]),
     "sq_gemm_mxfp4": (_I, [_P, _P, _I, _P, _P, _I64, _I64, _I64, _P, _I, _P]),
+    # the microscaled cache (include/sq_kv.h)
+    "sq_rope_quantize_kv_mx": (_I, [_P, _STRIDE_P, _P, _STRIDE_P, _P, _STRIDE_P, _I, _I64, _I64, _P,
+                                    _P, _I64, ctypes.c_double, _I, _P, _P, _P, _CACHE_P, _P, _P]),
+    "sq_dequantize_kv_mx": (_I, [_CACHE_P, _P, _I64, _I64, _P, _I64, _P, _P, _I, _P]),
+    "sq_attention_kv_mx": (_I, [_P, _STRIDE_P, _I, _I64, _I64, _CACHE_P, _P, _I64, _I64, _P, _P, _I64,
+                                _F, _I, _I64, _P, _P, ctypes.c_size_t, _P]),
+    "sq_attention_kv_mx_workspace": (ctypes.c_size_t, [_I64, _I64, _CACHE_P, _I64, _I64, _I64]),
     # coverage entry point (include/sq_mx_test.h): the pipelined product's block shape forced
     "sq_gemm_mxfp4_tile": (_I, [_P, _P, _I, _P, _P, _I64, _I64, _I64, _P, _I, _P, _I]),
     # coverage entry points (include/sq_test.h): the tiled GEMM's block shape forced
@@ -656,4 +678,247 @@ def gemm_mxfp4(xq, x_scale, wq, w_scale, x_fmt=SQ_MX_E2M1, out_dtype=None, out=N
         _mx_call("sq_gemm_mxfp4", (xq, x_scale, wq, w_scale, y), args, stream)
     else:
         _mx_call("sq_gemm_mxfp4_tile", (xq, x_scale, wq, w_scale, y), args, stream, int(tile))
+    return y
+
+
+# ------------------------------- a microscaled cache of keys and values
+
+def new_kv_cache_mx(pages, heads, page, dim, fmt=SQ_MX_E2M1, device="cuda"):
+    """An empty cache of `pages` pages of `page` tokens: (kq, ks, vq, vs), codes
+    uint8 [pages, heads, page, dim/2] or [.., dim] and scale bytes [.., dim/32]
+    of keys and values."""
+    if dim % 32:
+        raise ValueError(f"heads of {dim} channels: a multiple of 32 is needed")
+    torch = _torch()
+
+    def zeros(n):
+        return torch.zeros((pages, heads, page, n), dtype=torch.uint8, device=device)
+
+    return (zeros(_mx_codes(fmt, dim)), zeros(dim // 32), zeros(_mx_codes(fmt, dim)), zeros(dim // 32))
+
+
+def rope_frequencies(rotary, base=10000.0, scaling=None, factor=1.0, original=None, fast=32.0,
+                     slow=1.0, device="cuda"):
+    """(inv_freq fp64 [rotary/2], amplitude) of rotary positions for
+    rope_quantize_kv_mx: base^(-2 i / rotary), for contexts `factor` times the
+    `original` length by `scaling`
+      None      as they are
+      "linear"  positions divided by the factor
+      "ntk"     the base raised so that the slowest frequency is divided by it
+      "yarn"    frequencies that turn fewer than `slow` times in the original
+                length divided by the factor, those that turn more than `fast`
+                times kept, a ramp between; amplitude 0.1 ln(factor) + 1"""
+    if rotary < 2 or rotary % 2:
+        raise ValueError(f"{rotary} rotated channels: an even number is needed")
+    if scaling not in (None, "linear", "ntk", "yarn"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    if not (base > 0 and factor >= 1):
+        raise ValueError(f"base {base}, factor {factor}: base > 0 and factor >= 1 are needed")
+    if scaling == "yarn" and not (original and original > 0 and fast > slow):
+        raise ValueError("yarn needs the original length, and fast > slow")
+    amplitude = 1.0
+    if scaling == "ntk" and rotary > 2:
+        base = base * factor ** (rotary / (rotary - 2.0))
+    freq = [float(base) ** (-2.0 * i / rotary) for i in range(rotary // 2)]
+    if scaling == "linear":
+        freq = [f / factor for f in freq]
+    elif scaling == "yarn":
+        amplitude = 0.1 * math.log(factor) + 1.0
+        for i, f in enumerate(freq):
+            turns = original * f / (2.0 * math.pi)
+            keep = min(1.0, max(0.0, (turns - slow) / (fast - slow)))
+            freq[i] = f * keep + f / factor * (1.0 - keep)
+    torch = _torch()
+    return torch.tensor(freq, dtype=torch.float64, device=device), amplitude
+
+
+def _kv_cache(cache, fmt):
+    """The C form of a cache (kq, ks, vq, vs)."""
+    u8 = _torch().uint8
+    kq, ks, vq, vs = cache
+    for t, name in ((kq, "cached keys"), (ks, "the keys' scales"), (vq, "cached values"),
+                    (vs, "the values' scales")):
+        _mx_check(t, name, (u8,), 4)
+    shape, blocks = kq.shape, ks.shape
+    dim = blocks[3] * 32
+    if (vq.shape != shape or vs.shape != blocks or shape[:3] != blocks[:3]
+            or shape[3] != _mx_codes(fmt, dim)):
+        raise ValueError(f"cache of codes {tuple(shape)}, {tuple(vq.shape)} and scales "
+                         f"{tuple(blocks)}, {tuple(vs.shape)}: they disagree")
+    return _KvCache(kq.data_ptr(), ks.data_ptr(), vq.data_ptr(), vs.data_ptr(), shape[0], shape[1],
+                    shape[2], dim, fmt)
+
+
+def _kv_rows(x, name, dim, dtypes):
+    """(pointer, strides) of rows [T, heads, dim], each dense."""
+    if not (x.is_cuda and x.dtype in dtypes and x.dim() == 3 and x.stride(2) == 1):
+        if not x.is_cuda:
+            raise ValueError(f"{name} must be a GPU tensor")
+        if x.dtype not in dtypes:
+            raise ValueError(f"{name}: dtype {x.dtype} not in {tuple(dtypes)}")
+        raise ValueError(f"{name} must be [tokens, heads, {dim}] with dense rows")
+    if x.shape[2] != dim:
+        raise ValueError(f"{name} has rows of {x.shape[2]} channels, the cache of {dim}")
+    return x.data_ptr(), _STRIDES(x.stride(0), x.stride(1))
+
+
+def _kv_ints(t, name, dtype, shape):
+    """The pointer of an integer tensor of this shape, or None."""
+    if t is None:
+        return None
+    if not (t.is_cuda and t.dtype == dtype and t.is_contiguous() and t.shape == shape):
+        _check(t, name, (dtype,), len(shape))
+        raise ValueError(f"{name} {tuple(t.shape)} is not {tuple(shape)}")
+    return t.data_ptr()
+
+
+def _kv_mul(t, name, heads, dim):
+    """The pointer of fp32 multipliers [heads, dim] (or as one vector), or None."""
+    if t is None:
+        return None
+    if not (t.is_cuda and t.dtype == _torch_mod.float32 and t.is_contiguous()):
+        _check(t, name, (_torch_mod.float32,))
+    if t.shape != (heads, dim) and t.shape != (heads * dim,):
+        raise ValueError(f"{name} {tuple(t.shape)} is not {(heads, dim)}")
+    return t.data_ptr()
+
+
+def _kv_result(out, name, shape, dtype, device, stream):
+    """A dense output [tokens, heads, dim]: `out`, checked, or a new one."""
+    if out is None:
+        rows, heads, dim = shape
+        return _mx_empty(rows, heads * dim, dtype, device, stream).view(shape)
+    if not (out.is_cuda and out.dtype == dtype and out.is_contiguous() and out.shape == shape):
+        _check(out, name, (dtype,), 3)
+        raise ValueError(f"{name} {tuple(out.shape)} is not {tuple(shape)}")
+    return out
+
+
+def rope_quantize_kv_mx(q, k, v, slots, cache, fmt=SQ_MX_E2M1, positions=None, inv_freq=None,
+                        amplitude=1.0, layout=SQ_ROPE_HALF, q_mul=None, k_mul=None, out=None,
+                        stream=None):
+    """Rotary positions, and keys and values quantized into the cache: rows of
+    k and v [T, heads, dim] go to slots [T] int64 (page * page size + place;
+    others, as -1, are not written), the rotated q [T, q_heads, dim] (None: keys
+    and values alone) is returned.  positions [T] int64 and inv_freq fp64
+    [rotary/2] (rope_frequencies; None: nothing is rotated), the first `rotary`
+    channels; q_mul, k_mul fp32 [heads, dim]: smoothing, after the rotation."""
+    c = _kv_cache(cache, fmt)
+    heads, dim = c.heads, c.dim
+    dt = k.dtype
+    kp, k_stride = _kv_rows(k, "k", dim, _dt_codes)
+    vp, v_stride = _kv_rows(v, "v", dim, (dt,))
+    T = k.shape[0]
+    if k.shape[1] != heads or v.shape != k.shape:
+        raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)} do not fit a cache of {heads} heads")
+    i64 = _torch_mod.int64
+    if slots is None:
+        raise ValueError("slots are needed")
+    sp = _kv_ints(slots, "slots", i64, (T,))
+    rotary, fp, pp = 0, None, None
+    if inv_freq is not None:
+        if positions is None:
+            raise ValueError("positions are needed")
+        pp = _kv_ints(positions, "positions", i64, (T,))
+        _mx_check(inv_freq, "inv_freq", (_torch_mod.float64,), 1)
+        rotary, fp = 2 * inv_freq.shape[0], inv_freq.data_ptr()
+        if rotary > dim or rotary % 16:
+            raise ValueError(f"{rotary} rotated channels: a multiple of 16 up to {dim} is needed")
+    qp, q_stride, q_heads, y = None, None, 0, None
+    if q is not None:
+        qp, q_stride = _kv_rows(q, "q", dim, (dt,))
+        q_heads = q.shape[1]
+        if q.shape[0] != T:
+            raise ValueError(f"q has {q.shape[0]} tokens, k {T}")
+        y = _kv_result(out, "out", (T, q_heads, dim), dt, q.device, stream)
+    elif q_mul is not None or out is not None:
+        raise ValueError("q_mul and out need q")
+    qm, km = _kv_mul(q_mul, "q_mul", q_heads, dim), _kv_mul(k_mul, "k_mul", heads, dim)
+    _mx_call("sq_rope_quantize_kv_mx",
+             (k, v, q, slots, positions if rotary else None, inv_freq, q_mul, k_mul, y) + tuple(cache),
+             (qp, q_stride, kp, k_stride, vp, v_stride, _dt_codes[dt], T, q_heads, pp, fp, rotary,
+              amplitude, layout, qm, km, sp, c, _ptr(y)), stream)
+    return y
+
+
+def dequantize_kv_mx(cache, table, cu, total, fmt=SQ_MX_E2M1, out_dtype=None, out=None, stream=None):
+    """(k, v) [total, heads, dim]: the values (fp16 unless out_dtype says
+    otherwise) of cached tokens, sequence after sequence.  table int32 [B,
+    width]: each sequence's pages; cu int32 [B + 1]: where each begins in the
+    result; rows from cu[B] on are left as they were."""
+    c = _kv_cache(cache, fmt)
+    i32 = _torch_mod.int32
+    _mx_check(table, "table", (i32,), 2)
+    B, width = table.shape
+    if cu is None:
+        raise ValueError("cu is needed")
+    cp = _kv_ints(cu, "cu", i32, (B + 1,))
+    dtype = out_dtype or _torch_mod.float16
+    if dtype not in _dt_codes:
+        raise ValueError(f"out_dtype {dtype} not in {tuple(_dt_codes)}")
+    shape = (int(total), c.heads, c.dim)
+    if shape[0] < 0:
+        raise ValueError(f"total {total}")
+    if out is not None:
+        dtype = out[0].dtype if out_dtype is None else dtype
+        if dtype not in _dt_codes:
+            raise ValueError(f"out: dtype {dtype} not in {tuple(_dt_codes)}")
+    k = _kv_result(None if out is None else out[0], "out", shape, dtype, table.device, stream)
+    v = _kv_result(None if out is None else out[1], "out", shape, dtype, table.device, stream)
+    _mx_call("sq_dequantize_kv_mx", (table, cu, k, v) + tuple(cache),
+             (c, table.data_ptr(), B, width, cp, shape[0], k.data_ptr(), v.data_ptr(),
+              _dt_codes[dtype]), stream)
+    return k, v
+
+
+def attention_kv_mx_workspace(T, q_heads, cache, B, width, max_q, fmt=SQ_MX_E2M1) -> int:
+    """Bytes of workspace of such an attention_kv_mx call."""
+    return int(lib().sq_attention_kv_mx_workspace(T, q_heads, _kv_cache(cache, fmt), B, width, max_q))
+
+
+def attention_kv_mx(q, cache, table, seq_lens, cu_q=None, fmt=SQ_MX_E2M1, max_q=None, scale=None,
+                    causal=True, window=0, out=None, workspace=None, stream=None):
+    """Attention of q [T, q_heads, dim] (fp16 or bf16) over the cache: y of its
+    shape.  seq_lens int32 [B]: each sequence's cached tokens, the queries' own
+    keys among them; cu_q int32 [B + 1]: where each sequence's queries begin
+    (None: one query a sequence).  table int32 [B, width].  max_q: an upper
+    bound of a sequence's queries (T without it).  scale: 1 / sqrt(dim) unless
+    given.  window > 0: a query sees that many keys at the most, itself the
+    last.  A query that sees no key gets 0.  workspace: attention_kv_mx_workspace
+    bytes (uint8), used by this call alone while it runs; allocated without it."""
+    c = _kv_cache(cache, fmt)
+    dim = c.dim
+    torch = _torch_mod
+    qp, q_stride = _kv_rows(q, "q", dim, (torch.float16, torch.bfloat16))
+    T, q_heads = q.shape[0], q.shape[1]
+    if q_heads == 0 or q_heads % c.heads:
+        raise ValueError(f"{q_heads} query heads do not share {c.heads} key heads evenly")
+    i32 = torch.int32
+    _mx_check(table, "table", (i32,), 2)
+    B, width = table.shape
+    if seq_lens is None:
+        raise ValueError("seq_lens are needed")
+    lp, cp = _kv_ints(seq_lens, "seq_lens", i32, (B,)), _kv_ints(cu_q, "cu_q", i32, (B + 1,))
+    if cu_q is None:
+        if T != B:
+            raise ValueError(f"{T} queries for {B} sequences need cu_q")
+        max_q = 1
+    elif max_q is None:
+        max_q = T
+    elif max_q < 1:
+        raise ValueError(f"max_q {max_q}")
+    if scale is None:
+        scale = dim ** -0.5
+    if window < 0:
+        raise ValueError(f"window {window}")
+    y = _kv_result(out, "out", (T, q_heads, dim), q.dtype, q.device, stream)
+    need = lib().sq_attention_kv_mx_workspace(T, q_heads, c, B, width, max_q)
+    if workspace is None:
+        workspace = _mx_empty(1, need, torch.uint8, q.device, stream)
+    else:
+        _check(workspace, "workspace", (torch.uint8,))
+    _mx_call("sq_attention_kv_mx", (q, table, seq_lens, cu_q, y, workspace) + tuple(cache),
+             (qp, q_stride, _dt_codes[q.dtype], T, q_heads, c, table.data_ptr(), B, width, lp, cp,
+              max_q, scale, 1 if causal else 0, window, y.data_ptr(), workspace.data_ptr(),
+              workspace.numel(), ), stream)
     return y

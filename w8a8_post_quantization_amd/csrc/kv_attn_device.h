@@ -1,0 +1,150 @@
+// What the attention kernels over the microscaled cache share: a sequence's
+// keys and queries, the matrix instructions by type, non-finite values.
+#pragma once
+
+#include "kv_device.h"
+
+namespace sq {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+// Finite, and below every score: the running maximum of a row that has seen no
+// key yet.
+constexpr float kNoMax = -3.402823466e38f;
+
+// C += A B of 16 x 16 x 32: lane l holds A[l % 16][8 (l / 16) ..], B[..][l % 16]
+// of the same eight inner indices, C[4 (l / 16) ..][l % 16].
+template <int DT>
+__device__ __forceinline__ f32x4 mfma16(const uint4 &a, const uint4 &b, f32x4 c) {
+    if constexpr (DT == BF16)
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                       __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
+                                                      __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
+// The same of 32 x 32 x 16: A[l % 32][8 (l / 32) ..], B[..][l % 32], C[i % 4 +
+// 8 (i / 4) + 4 (l / 32)][l % 32].
+template <int DT>
+__device__ __forceinline__ f32x16 mfma32(const uint4 &a, const uint4 &b, f32x16 c) {
+    if constexpr (DT == BF16)
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
+                                                       __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a),
+                                                      __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
+// Two fp32 -> one word of the 16-bit type, to nearest even.
+template <int DT>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+    if constexpr (DT == BF16) {
+        const bf16x2 v = {(__bf16)lo, (__bf16)hi};
+        return __builtin_bit_cast(uint32_t, v);
+    } else {
+        const f16x2 v = {(_Float16)lo, (_Float16)hi};
+        return __builtin_bit_cast(uint32_t, v);
+    }
+}
+
+// The halves of a word that are infinite or NaN: as 1.0 of the type where the
+// value is +infinity or NaN (`up`), -infinity or NaN (`down`); the word with
+// those halves 0 is returned.
+template <int DT>
+__device__ __forceinline__ uint32_t split_nonfinite(uint32_t w, uint32_t &up, uint32_t &down) {
+    constexpr uint32_t kTop = DT == BF16 ? 0x7f80u : 0x7c00u, kOne = DT == BF16 ? 0x3f80u : 0x3c00u;
+    uint32_t keep = w;
+    up = down = 0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t x = (w >> (16 * h)) & 0xffffu, mag = x & 0x7fffu;
+        if (mag >= kTop) {
+            if (mag > kTop || x < 0x8000u) up |= kOne << (16 * h);
+            if (mag > kTop || x >= 0x8000u) down |= kOne << (16 * h);
+            keep &= ~(0xffffu << (16 * h));
+        }
+    }
+    return keep;
+}
+
+// Words that hold N bytes of codes, as loaded.
+template <int N> struct Words { uint32_t w[N < 4 ? 1 : N / 4]; };
+template <int N>
+__device__ __forceinline__ Words<N> load_codes(const uint8_t *p) {
+    Words<N> r;
+    if constexpr (N == 2) {
+        r.w[0] = *reinterpret_cast<const uint16_t *>(p);
+    } else if constexpr (N == 4) {
+        r.w[0] = *reinterpret_cast<const uint32_t *>(p);
+    } else if constexpr (N == 8) {
+        const uint2 v = *reinterpret_cast<const uint2 *>(p);
+        r.w[0] = v.x;
+        r.w[1] = v.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < N / 16; ++i) {
+            const uint4 v = reinterpret_cast<const uint4 *>(p)[i];
+            r.w[4 * i] = v.x;
+            r.w[4 * i + 1] = v.y;
+            r.w[4 * i + 2] = v.z;
+            r.w[4 * i + 3] = v.w;
+        }
+    }
+    return r;
+}
+
+// The q-th pair of codes among a lane's words.
+template <int FMT, int DT, int N>
+__device__ __forceinline__ uint32_t pair_of(const Words<N> &c, int q, float s) {
+    if constexpr (FMT == E2M1) {
+        const uint32_t w = c.w[q >> 2];
+        switch (q & 3) {
+            case 0: return e2m1_pair<DT, 0>(w, s);
+            case 1: return e2m1_pair<DT, 1>(w, s);
+            case 2: return e2m1_pair<DT, 2>(w, s);
+            default: return e2m1_pair<DT, 3>(w, s);
+        }
+    } else {
+        return q & 1 ? e4m3_pair<DT, true>(c.w[q >> 1], s) : e4m3_pair<DT, false>(c.w[q >> 1], s);
+    }
+}
+
+// One sequence's part in the call.  lo .. hi: the keys that any query sees.
+struct KvSeq {
+    int q0, nq, nk, lo, hi;
+    bool over;  // longer than its row of the table: its queries get NaN
+};
+
+// What a row's weighted values are multiplied by: nothing seen gives 0.
+__device__ __forceinline__ float row_factor(float sum, bool over) {
+    if (over) return __uint_as_float(0x7fc00000u);
+    return sum == 0.0f ? 0.0f : 1.0f / sum;
+}
+
+__device__ __forceinline__ KvSeq kv_seq(const KvAttention &a, int b) {
+    KvSeq s;
+    const int T = (int)a.T;
+    int q0 = b, q1 = b + 1;
+    if (a.cu_q) {
+        q0 = a.cu_q[b];
+        q1 = a.cu_q[b + 1];
+        q0 = q0 < 0 ? 0 : q0 > T ? T : q0;
+        q1 = q1 < q0 ? q0 : q1 > T ? T : q1;
+    }
+    s.q0 = q0;
+    s.nq = q1 - q0;
+    const int cap = (int)(a.width << a.cache.page_log);
+    const int len = a.seq_lens[b];
+    s.over = len > cap;
+    s.nk = len < 0 ? 0 : s.over ? cap : len;
+    s.hi = s.nk;
+    const int64_t lo = a.window ? (int64_t)s.nk - s.nq + 1 - a.window : 0;
+    s.lo = lo > 0 ? (int)lo : 0;
+    return s;
+}
+
+}  // namespace sq
