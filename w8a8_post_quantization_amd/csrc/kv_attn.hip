@@ -23,7 +23,7 @@
 namespace sq {
 
 constexpr int kTile = 128;       // keys of a unit of work: 32 for each of four waves
-constexpr int kMaxBlocks = 1024;
+constexpr int kMaxBlocks = 1024;  // (at most, whatever a CU holds)
 
 // What a block leaves in the workspace for the joining kernel.
 struct Part {
@@ -35,27 +35,44 @@ template <int D, int NT> struct PartSize {
     static constexpr int floats = rows * (D + 2);  // values, maxima, sums
 };
 
-// 32 keys' codes and scales as a lane loads them.
-template <int D, int FMT> struct Keys32 {
+// 32 keys' codes and scales in a wave's LDS ring: the keys' codes, the values',
+// then the keys' scales and the values', as they lie in the cache.
+template <int D, int FMT> struct Tile32 {
     static constexpr int NB = D / 32;
-    static constexpr int KN = NB * (FMT == E2M1 ? 4 : 8);   // code bytes of a key, a quarter of its channels
-    static constexpr int KS = NB < 4 ? 1 : NB / 4;          // scale bytes of those
-    static constexpr int VN = FMT == E2M1 ? D / 32 : D / 16;  // code bytes of a value, a sixteenth of its channels
-    Words<KN> k[2];
-    uint32_t ks[2][KS];
-    Words<VN> v[8];
-    uint32_t vs[8];
+    static constexpr int RB = FMT == E2M1 ? D / 2 : D;        // code bytes of a row
+    static constexpr int KN = RB / 4;                         // of those, a lane's of a key: a quarter
+    static constexpr int KS = NB < 4 ? 1 : NB / 4;            // scale bytes of a quarter
+    static constexpr int VN = RB / 16;                        // a lane's of a value: a sixteenth
+    static constexpr int codes = 32 * RB, scales = 32 * NB;
+    static constexpr int scale_loads = 2 * scales > 256 ? 2 * scales / 256 : 1;
+    static constexpr int loads = 2 * codes / 1024 + scale_loads;
+    static constexpr int bytes = 2 * codes + 256 * scale_loads;
+    // As many tiles in flight as a CU's LDS has room for with 3 blocks (2 where
+    // a tile is 8 KB, 1 where it is 17 KB).
+    static constexpr int stages = bytes < 4096 ? 4 : bytes < 8192 ? 3 : 2;
 };
+constexpr int kCus = 256;
+// Blocks of the kernel on a CU: LDS allows 3, 2 or 1 of them; with two column
+// groups registers allow 2, of 256 channels 1.
+constexpr int blocks_per_cu(int dim, int fmt, int nt) {
+    const int row = fmt == E2M1 ? dim / 2 : dim;  // code bytes: 32 to 256
+    const int n = row <= 64 ? 3 : row <= 128 ? 2 : 1;
+    return nt == 1 ? n : dim == 256 ? 1 : n < 2 ? n : 2;
+}
 
 template <int D, int FMT, int DT, int NT>
-__global__ __launch_bounds__(256) void kv_attn_kernel(const KvAttention a, int rows_max) {
-    constexpr int NB = D / 32, J = D / 16;  // blocks of a row; channel tiles
-    using Raw = Keys32<D, FMT>;
-    constexpr int RB = FMT == E2M1 ? D / 2 : D;  // code bytes of a row
-    __shared__ int64_t s_pre[257];
+__global__ __launch_bounds__(256, (blocks_per_cu(D, FMT, NT))) void kv_attn_kernel(
+    const KvAttention a, int rows_max, const int32_t *__restrict__ tables) {
+    using L = Tile32<D, FMT>;
+    constexpr int NB = L::NB, RB = L::RB, J = D / 16;  // blocks, code bytes of a row; channel tiles
+    constexpr int kRing = 4 * L::stages * L::bytes, kJoin = 2 * NT * J * 64 * 16;
     __shared__ int s_at[2];
     __shared__ float s_m[4][16 * NT], s_l[4][16 * NT];
-    __shared__ f32x4 s_o[2][NT * J][64];
+    // first the sequences' units, then the waves' rings, and (an item's keys
+    // read) the join of the waves' sums
+    __shared__ __attribute__((aligned(1024))) uint8_t s_ring[kRing > kJoin ? kRing : kJoin];
+    int64_t *const s_pre = reinterpret_cast<int64_t *>(s_ring), *const s_wave = s_pre + 257;
+    const auto s_o = reinterpret_cast<f32x4(*)[NT * J][64]>(s_ring);
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -75,15 +92,17 @@ __global__ __launch_bounds__(256) void kv_attn_kernel(const KvAttention a, int r
     {
         int64_t sum = 0;
         for (int i = 0; i < per_thread && b_first + i < a.B; ++i) sum += units_of(kv_seq(a, b_first + i));
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) {
+            const int64_t v = __shfl_up(sum, off, 64);
+            if (lane >= off) sum += v;
+        }
+        if (lane == 63) s_wave[wave] = sum;
+        __syncthreads();
+        for (int w = 0; w < wave; ++w) sum += s_wave[w];
         s_pre[tid + 1] = sum;
         if (tid == 0) s_pre[0] = 0;
         __syncthreads();
-        for (int off = 1; off < 256; off <<= 1) {
-            const int64_t v = tid >= off ? s_pre[tid + 1 - off] : 0;
-            __syncthreads();
-            s_pre[tid + 1] += v;
-            __syncthreads();
-        }
     }
     const int64_t total = s_pre[256] * heads;
     const int64_t share = (total + gridDim.x - 1) / gridDim.x;
@@ -123,6 +142,8 @@ __global__ __launch_bounds__(256) void kv_attn_kernel(const KvAttention a, int r
     int tile = rem - h * units;
 
     const float c = a.scale * 1.44269504088896341f;
+    uint8_t *const ring = s_ring + wave * L::stages * L::bytes;
+    const uint32_t ring_at = (uint32_t)(uintptr_t)(lds_void_t *)ring;
     for (int64_t u = u0; u < u1;) {
         const int count = (int)(u1 - u < units - tile ? u1 - u : units - tile);
         const int rows = seq.nq * group;
@@ -162,32 +183,83 @@ __global__ __launch_bounds__(256) void kv_attn_kernel(const KvAttention a, int r
             for (int j = 0; j < J; ++j) o[nt][j] = f32x4{0, 0, 0, 0};
         }
 
-        const int32_t *const table = a.table + (int64_t)b * a.width;
+        const int32_t *const table = tables + (int64_t)b * a.width;
         const int g_last = (seq.hi - 1) >> 4;
-        const auto load = [&](int t, Raw &r) {
+        // A tile's loads go to LDS by themselves, so that tiles in flight take no
+        // registers.  Its pages are looked up a tile ahead; whether each was in
+        // the cache is kept as two bits a tile, the newest lowest.
+        int page[2];
+        uint32_t missing = 0;
+        const auto look_up = [&](int t) {
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                int grp = (t >> 4) + half;
-                grp = __builtin_amdgcn_readfirstlane(grp < g_last ? grp : g_last);
-                int64_t page = table[grp >> (plog - 4)];
-                const bool held = page >= 0 && page < a.cache.pages;
-                page = held ? page : 0;
-                const int64_t row = kv_row(a.cache, page, h, (grp & ((1 << (plog - 4)) - 1)) << 4);
-                const uint8_t *kq = a.cache.kq + row * RB + n16 * RB + g * Raw::KN;
-                r.k[half] = load_codes<Raw::KN>(kq);
-                const uint8_t *ks = a.cache.ks + row * NB + n16 * NB + g * NB / 4;
-#pragma unroll
-                for (int i = 0; i < Raw::KS; ++i) r.ks[half][i] = held ? ks[i] : 255u;
-                const uint8_t *vq = a.cache.vq + row * RB + 4 * g * RB + n16 * Raw::VN;
-                const uint8_t *vs = a.cache.vs + row * NB + 4 * g * NB + n16 * NB / 16;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    r.v[4 * half + i] = load_codes<Raw::VN>(vq + i * RB);
-                    r.vs[4 * half + i] = held ? vs[i * NB] : 255u;
-                }
+                const int grp = (t >> 4) + half;
+                page[half] = table[__builtin_amdgcn_readfirstlane(grp < g_last ? grp : g_last) >> (plog - 4)];
             }
         };
-        const auto compute = [&](Raw &r, int t) {
+        const auto load = [&](int t, int slot) {
+            int64_t row[2];
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int grp = (t >> 4) + half;
+                const int in_page = __builtin_amdgcn_readfirstlane((grp < g_last ? grp : g_last) & ((1 << (plog - 4)) - 1));
+                const int p = __builtin_amdgcn_readfirstlane(page[half]);
+                const bool held = p >= 0 && p < a.cache.pages;
+                missing = missing << 1 | (held ? 0 : 1);
+                row[half] = kv_row(a.cache, held ? p : 0, h, in_page << 4);
+            }
+            look_up(t + kTile);
+            const int8_t *from[2 * L::codes / 1024];
+#pragma unroll
+            for (int i = 0; i < 2 * L::codes / 1024; ++i) {
+                const uint8_t *q = i < L::codes / 1024 ? a.cache.kq : a.cache.vq;
+                const int at = i * 1024 % L::codes;
+                if constexpr (16 * RB >= 1024) {
+                    from[i] = (const int8_t *)(q + row[at / (16 * RB)] * RB) + (uint32_t)(at % (16 * RB) + lane * 16);
+                } else {  // (both groups of 16 keys in one load)
+                    from[i] = (const int8_t *)(q + (lane < 32 ? row[0] : row[1]) * RB) + (uint32_t)(lane % 32 * 16);
+                }
+            }
+            const uint32_t to = ring_at + slot * L::bytes;
+            lds_dma_run<2 * L::codes / 1024, true>(from, to);
+#pragma unroll
+            for (int i = 0; i < L::scale_loads; ++i) {
+                constexpr int W = L::scales / 4;  // words of 32 keys' scales
+                const int w = (i * 64 + lane) % (2 * W);
+                const uint8_t *e = w < W ? a.cache.ks : a.cache.vs;
+                lds_dma4(e + (w % W < W / 2 ? row[0] : row[1]) * NB + w % (W / 2) * 4, to + 2 * L::codes + i * 256);
+            }
+        };
+        const auto compute = [&](int t, int slot, uint32_t gone) {
+            const bool masked = t < all_lo || t + 32 > all_hi || t + 32 > te;
+            const uint8_t *const kq = ring + slot * L::bytes, *const vq = kq + L::codes;
+            const uint8_t *const ks = vq + L::codes, *const vs = ks + L::scales;
+            Words<L::KN> k[2];
+            uint32_t ke[2][L::KS];
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                k[half] = load_codes<L::KN>(kq + (16 * half + n16) * RB + g * L::KN);
+#pragma unroll
+                for (int i = 0; i < L::KS; ++i) ke[half][i] = ks[(16 * half + n16) * NB + g * NB / 4 + i];
+            }
+            Words<L::VN> v[8];
+            uint32_t ve[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int key = 16 * (i >> 2) + 4 * g + (i & 3);
+                v[i] = load_codes<L::VN>(vq + key * RB + n16 * L::VN);
+                ve[i] = vs[key * NB + n16 * NB / 16];
+            }
+            if (gone) {  // pages that are not in the cache: NaN
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const uint32_t nan = gone >> (1 - half) & 1 ? 255u : 0u;
+#pragma unroll
+                    for (int i = 0; i < L::KS; ++i) ke[half][i] |= nan;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) ve[4 * half + i] |= nan;
+                }
+            }
             f32x4 st[NT][2];
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
@@ -195,46 +267,54 @@ __global__ __launch_bounds__(256) void kv_attn_kernel(const KvAttention a, int r
                 for (int nt = 0; nt < NT; ++nt) st[nt][half] = f32x4{0, 0, 0, 0};
 #pragma unroll
                 for (int s = 0; s < NB; ++s) {
-                    const float sc = e8m0(r.ks[half][NB < 4 ? 0 : s / 4]);
-                    const uint4 kf = codes8_to_16<FMT, DT>(&r.k[half].w[s * (FMT == E2M1 ? 1 : 2)], sc);
+                    const float sc = e8m0(ke[half][NB < 4 ? 0 : s / 4]);
+                    const uint4 kf = codes8_to_16<FMT, DT>(&k[half].w[s * (FMT == E2M1 ? 1 : 2)], sc);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) st[nt][half] = mfma16<DT>(kf, qf[nt][s], st[nt][half]);
                 }
             }
-            const bool masked = t < all_lo || t + 32 > all_hi || t + 32 > te;
+            uint32_t apart = 0;
             if (masked) {
+                asm volatile("");  // (a branch, not selects)
                 // keys that no row sees (behind the last, before the window) are
                 // taken as 0: what their place holds may be anything
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int key = t + 16 * (i >> 2) + 4 * g + (i & 3);
-                    if (key < seq.lo || key >= te) {
-                        r.vs[i] = 0;
-                        r.v[i] = Words<Raw::VN>{};
+                    const bool none = key < seq.lo || key >= te;
+                    // A weight of 0 does not keep an infinity or NaN from a row
+                    // that must not see it: such keys are taken on their own.
+                    const bool alone = !none && seq.nq > 1 && may_be_nonfinite<FMT, DT>(v[i], ve[i]);
+                    const uint64_t who = __ballot(alone);
+                    // (a key is the lanes of one g; the whole key is set apart)
+                    const bool mine = (who >> (16 * g) & 0xffff) != 0;
+#pragma unroll
+                    for (int n = 0; n < 4; ++n)
+                        if (who >> (16 * n) & 0xffff) apart |= 1u << (16 * (i >> 2) + 4 * n + (i & 3));
+                    if (none || mine) {
+                        ve[i] = 0;
+                        v[i] = Words<L::VN>{};
                     }
                 }
             }
-            uint4 pf[NT], seen[NT];
+            apart = __builtin_amdgcn_readfirstlane(apart);
+            uint4 pf[NT];
+            float x[NT][8];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                float x[8];
                 float top = -INFINITY;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = st[nt][i >> 2][i & 3] * c;
+                for (int i = 0; i < 8; ++i) x[nt][i] = st[nt][i >> 2][i & 3] * c;
                 if (masked) {
-                    uint32_t v[8];
+                    asm volatile("");
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const int key = t + 16 * (i >> 2) + 4 * g + (i & 3);
-                        const bool vis = key >= r_lo[nt] && key < r_hi[nt] && key < te;
-                        x[i] = vis ? x[i] : -INFINITY;
-                        v[i] = vis ? (DT == BF16 ? 0x3f80u : 0x3c00u) : 0u;
+                        if (key < r_lo[nt] || key >= r_hi[nt] || key >= te) x[nt][i] = -INFINITY;
                     }
-                    seen[nt] = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16,
-                                          v[6] | v[7] << 16);
                 }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) top = fmaxf(top, x[i]);
+                for (int i = 0; i < 8; ++i) top = fmaxf(top, x[nt][i]);
                 // The maximum may trail the true one by 8 (weights up to 256):
                 // rows are rescaled only where it is passed by more.
                 if (__any(top > m[nt] + 8.0f)) {
@@ -249,71 +329,82 @@ __global__ __launch_bounds__(256) void kv_attn_kernel(const KvAttention a, int r
                 }
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    x[i] = __builtin_amdgcn_exp2f(x[i] - m[nt]);
-                    l[nt] += x[i];
+                    x[nt][i] = __builtin_amdgcn_exp2f(x[nt][i] - m[nt]);
+                    l[nt] += x[nt][i];
                 }
-                pf[nt] = make_uint4(pack16<DT>(x[0], x[1]), pack16<DT>(x[2], x[3]),
-                                    pack16<DT>(x[4], x[5]), pack16<DT>(x[6], x[7]));
+                pf[nt] = make_uint4(pack16<DT>(x[nt][0], x[nt][1]), pack16<DT>(x[nt][2], x[nt][3]),
+                                    pack16<DT>(x[nt][4], x[nt][5]), pack16<DT>(x[nt][6], x[nt][7]));
             }
             float sc[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sc[i] = e8m0(r.vs[i]);
+            for (int i = 0; i < 8; ++i) sc[i] = e8m0(ve[i]);
 #pragma unroll
             for (int q = 0; q < J / 2; ++q) {
                 uint32_t w[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) w[i] = pair_of<FMT, DT>(r.v[i], q, sc[i]);
+                for (int i = 0; i < 8; ++i) w[i] = pair_of<FMT, DT>(v[i], q, sc[i]);
 #pragma unroll
                 for (int odd = 0; odd < 2; ++odd) {
                     const uint32_t sel = odd ? 0x07060302u : 0x05040100u;
-                    uint4 vf = make_uint4(__builtin_amdgcn_perm(w[1], w[0], sel), __builtin_amdgcn_perm(w[3], w[2], sel),
+                    const uint4 vf = make_uint4(__builtin_amdgcn_perm(w[1], w[0], sel), __builtin_amdgcn_perm(w[3], w[2], sel),
                                           __builtin_amdgcn_perm(w[5], w[4], sel), __builtin_amdgcn_perm(w[7], w[6], sel));
                     const int j = 2 * q + odd;
-                    if (masked && seq.nq > 1) {
-                        // A weight of 0 does not keep an infinity or NaN from a
-                        // row that must not see it: they are taken out, and
-                        // brought to the rows that see them by a product of ones.
-                        uint4 up, down;
-                        vf.x = split_nonfinite<DT>(vf.x, up.x, down.x);
-                        vf.y = split_nonfinite<DT>(vf.y, up.y, down.y);
-                        vf.z = split_nonfinite<DT>(vf.z, up.z, down.z);
-                        vf.w = split_nonfinite<DT>(vf.w, up.w, down.w);
-                        const uint32_t any = up.x | up.y | up.z | up.w | down.x | down.y | down.z | down.w;
-                        if (__any(any != 0)) {
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) {
-                                const f32x4 cu = mfma16<DT>(up, seen[nt], f32x4{0, 0, 0, 0});
-                                const f32x4 cd = mfma16<DT>(down, seen[nt], f32x4{0, 0, 0, 0});
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    if (cu[i] > 0) o[nt][j][i] += INFINITY;
-                                    if (cd[i] > 0) o[nt][j][i] -= INFINITY;
-                                }
-                            }
-                        }
-                    }
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) o[nt][j] = mfma16<DT>(vf, pf[nt], o[nt][j]);
                 }
             }
+            // (rare) The keys set apart, one at a time, for the rows that see them.
+            for (; apart; apart &= apart - 1) {
+                const int n = __builtin_ctz(apart), i = 4 * (n >> 4) + (n & 3), from = n16 + 16 * ((n >> 2) & 3);
+                const int key = t + n;
+                const uint32_t nan = gone >> (1 - (n >> 4)) & 1 ? 255u : 0u;
+                float w[NT];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float p = x[nt][0];
+#pragma unroll
+                    for (int z = 1; z < 8; ++z) p = z == i ? x[nt][z] : p;
+                    w[nt] = __shfl(p, from, 64);
+                }
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {  // J channels from J (4 g + z) on
+                    const Words<L::VN> c = load_codes<L::VN>(vq + n * RB + (4 * g + z) * L::VN);
+                    const uint32_t e = vs[n * NB + (4 * g + z) * NB / 16] | nan;
+#pragma unroll
+                    for (int j = 0; j < J; ++j) {
+                        const float val = half_of<DT>(pair_of<FMT, DT>(c, j >> 1, e8m0(e)), j & 1);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            if (key >= r_lo[nt] && key < r_hi[nt]) o[nt][j][z] += w[nt] * val;
+                    }
+                }
+            }
         };
-        {
-            Raw r0, r1;
-            int t = ta + 32 * wave;
-            if (t < te) load(t, r0);
-            while (t < te) {
-                if (t + kTile < te) load(t + kTile, r1);
-                compute(r0, t);
-                t += kTile;
-                if (t >= te) break;
-                if (t + kTile < te) load(t + kTile, r0);
-                compute(r1, t);
-                t += kTile;
+        const int t0 = ta + 32 * wave;
+        const int n_tiles = t0 < te ? (te - t0 + kTile - 1) / kTile : 0;
+        if (n_tiles) {
+            look_up(t0);
+            int slot = 0;  // of the next load
+            for (int i = 0; i < L::stages - 1 && i < n_tiles; ++i) load(t0 + i * kTile, slot++);
+            int read = 0;
+            for (int i = 0; i < n_tiles; ++i) {
+                const int more = n_tiles - 1 - i;
+                if (more >= L::stages - 1) {
+                    // (the slot's last reads have returned)
+                    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                    load(t0 + (i + L::stages - 1) * kTile, slot);
+                    slot = slot + 1 == L::stages ? 0 : slot + 1;
+                }
+                const int later = more < L::stages - 1 ? more : L::stages - 1;
+                wait_stages<L::stages - 1, L::loads>(later);
+                asm volatile("" ::: "memory");
+                compute(t0 + i * kTile, read, missing >> (2 * later) & 3);
+                read = read + 1 == L::stages ? 0 : read + 1;
             }
         }
 
         // Join the waves: one maximum, then the values of waves 2 and 3 into 0
-        // and 1, of 1 into 0.
+        // and 1, of 1 into 0.  (All loads to the rings have been waited for.)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             l[nt] += __shfl_xor(l[nt], 16, 64);
@@ -323,7 +414,7 @@ __global__ __launch_bounds__(256) void kv_attn_kernel(const KvAttention a, int r
                 s_l[wave][nt * 16 + n16] = l[nt];
             }
         }
-        __syncthreads();
+        __syncthreads();  // (the rings are read, too)
         float mx[NT], sum[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -424,38 +515,39 @@ __global__ __launch_bounds__(256) void kv_join_kernel(const KvAttention a) {
     if (p.last < 0 || r >= p.rows) return;
     const float *const parts = work + kMaxBlocks * sizeof(Part) / sizeof(float);
     __shared__ f32x4 s_o[W][Q];
-    __shared__ float s_m[W], s_l[W];
+    __shared__ float s_f[kMaxBlocks], s_red[4];
     const int d4 = threadIdx.x % Q, w = threadIdx.x / Q;
     const int first = blockIdx.x, n = p.last - first + 1;
-    float m = kNoMax, l = 0.0f;
+    // (the first block's part is its second: it begins the item)
+    const auto part = [&](int i) { return parts + (int64_t)((first + i) * 2 + (i == 0)) * PartSize<D, NT>::floats; };
+    const auto reduced = [&](float v, auto op) {
+#pragma unroll
+        for (int off = 32; off; off >>= 1) v = op(v, __shfl_xor(v, off, 64));
+        if ((threadIdx.x & 63) == 0) s_red[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = op(op(s_red[0], s_red[1]), op(s_red[2], s_red[3]));
+        __syncthreads();
+        return v;
+    };
+    float mx = kNoMax, sum = 0.0f;
+    for (int i = threadIdx.x; i < n; i += 256) {
+        s_f[i] = part(i)[16 * NT * D + r];
+        mx = fmaxf(mx, s_f[i]);
+    }
+    mx = reduced(mx, [](float x, float y) { return fmaxf(x, y); });
+    for (int i = threadIdx.x; i < n; i += 256) {
+        s_f[i] = __builtin_amdgcn_exp2f(s_f[i] - mx);
+        sum += part(i)[16 * NT * D + 16 * NT + r] * s_f[i];
+    }
+    sum = reduced(sum, [](float x, float y) { return x + y; });
     f32x4 o = {0, 0, 0, 0};
-    for (int i = w; i < n; i += W) {
-        // (the first block's part is its second: it begins the item)
-        const float *x = parts + (int64_t)((first + i) * 2 + (i == 0)) * PartSize<D, NT>::floats;
-        const float pm = x[16 * NT * D + r], pl = x[16 * NT * D + 16 * NT + r];
-        const f32x4 v = *reinterpret_cast<const f32x4 *>(x + r * D + 4 * d4);
-        const float mn = fmaxf(m, pm);
-        const float f = __builtin_amdgcn_exp2f(m - mn), e = __builtin_amdgcn_exp2f(pm - mn);
-        l = l * f + pl * e;
-        o = o * f + v * e;
-        m = mn;
-    }
+#pragma unroll 8
+    for (int i = w; i < n; i += W) o += *reinterpret_cast<const f32x4 *>(part(i) + r * D + 4 * d4) * s_f[i];
     s_o[w][d4] = o;
-    if (d4 == 0) {
-        s_m[w] = m;
-        s_l[w] = l;
-    }
     __syncthreads();
     if (w != 0) return;
-    float mx = s_m[0];
-    for (int i = 1; i < W; ++i) mx = fmaxf(mx, s_m[i]);
-    float sum = 0.0f;
-    f32x4 v = {0, 0, 0, 0};
-    for (int i = 0; i < W; ++i) {
-        const float e = __builtin_amdgcn_exp2f(s_m[i] - mx);
-        sum += s_l[i] * e;
-        v += s_o[i][d4] * e;
-    }
+    f32x4 v = o;
+    for (int i = 1; i < W; ++i) v += s_o[i][d4];
     const KvSeq seq = kv_seq(a, p.b);
     const float inv = row_factor(sum, seq.over);
     const int i = r / a.group;
@@ -469,13 +561,14 @@ struct Plan {
     int nt;             // column groups of 16 rows of the kernel above; 0: not used
     int rows_max;       // it takes the sequences of up to so many rows
     int64_t blocks;
-    int wr;             // row groups a wave of the tile kernel; 0: not used
+    int waves;          // of a block of the tile kernel, 32 rows each; 0: not used
     int splits;
     size_t tile_parts;  // where its parts begin in the workspace
     size_t bytes;
 };
 
-static Plan plan_attention(int64_t T, int q_heads, int heads, int dim, int B, int64_t keys, int64_t max_q) {
+static Plan plan_attention(int64_t T, int q_heads, int heads, int dim, int fmt, int B, int64_t keys,
+                           int64_t max_q) {
     Plan p = {};
     const int64_t group = q_heads / heads, most = max_q * group;
     // Up to 32 rows the first kernel has all. Of a call with longer sequences it
@@ -484,12 +577,13 @@ static Plan plan_attention(int64_t T, int q_heads, int heads, int dim, int B, in
     p.rows_max = (int)(most < 16 * p.nt ? most : 16 * p.nt);
     if (p.nt) {
         const int64_t units = (int64_t)B * heads * ((keys + 15 + kTile - 1) / kTile);
-        p.blocks = units < kMaxBlocks ? (units > 0 ? units : 1) : kMaxBlocks;
+        const int64_t most_blocks = (int64_t)kCus * blocks_per_cu(dim, fmt, p.nt);
+        p.blocks = units < most_blocks ? (units > 0 ? units : 1) : most_blocks;
         p.bytes = kMaxBlocks * sizeof(Part) + (size_t)p.blocks * 2 * 16 * p.nt * (dim + 2) * sizeof(float);
     }
     if (most > 32) {
-        p.wr = dim == 256 || most <= 128 ? 1 : 2;
-        const int64_t tiles = (T * group + 128 * p.wr - 1) / (128 * p.wr) * heads;
+        p.waves = dim == 256 || most <= 128 ? 4 : 8;
+        const int64_t tiles = (T * group + 32 * p.waves - 1) / (32 * p.waves) * heads;
         // few tiles: the keys of each are split over blocks
         int64_t splits = tiles >= 256 ? 1 : 512 / tiles;
         if (splits > (keys + 511) / 512) splits = (keys + 511) / 512;
@@ -500,13 +594,14 @@ static Plan plan_attention(int64_t T, int q_heads, int heads, int dim, int B, in
     return p;
 }
 
-size_t kv_attention_workspace(int64_t T, int q_heads, int heads, int dim, int B, int64_t keys, int64_t max_q) {
-    return plan_attention(T, q_heads, heads, dim, B, keys, max_q).bytes;
+size_t kv_attention_workspace(int64_t T, int q_heads, int heads, int dim, int fmt, int B, int64_t keys,
+                              int64_t max_q) {
+    return plan_attention(T, q_heads, heads, dim, fmt, B, keys, max_q).bytes;
 }
 
 template <int D, int FMT, int DT, int NT>
 static void launch_attn(const KvAttention &a, const Plan &p, hipStream_t stream) {
-    kv_attn_kernel<D, FMT, DT, NT><<<(unsigned)p.blocks, 256, 0, stream>>>(a, p.rows_max);
+    kv_attn_kernel<D, FMT, DT, NT><<<(unsigned)p.blocks, 256, 0, stream>>>(a, p.rows_max, a.table);
     if (p.blocks > 1)
         kv_join_kernel<D, DT, NT><<<dim3((unsigned)p.blocks, p.rows_max), 256, 0, stream>>>(a);
 }
@@ -529,15 +624,15 @@ static void launch_attn_d(const KvAttention &a, const Plan &p, int dt, hipStream
 }
 
 void launch_kv_attention(const KvAttention &a, int64_t max_q, int dt, hipStream_t stream) {
-    const Plan p = plan_attention(a.T, a.q_heads, a.cache.heads, a.cache.dim, a.B,
+    const Plan p = plan_attention(a.T, a.q_heads, a.cache.heads, a.cache.dim, a.cache.fmt, a.B,
                                   a.width << a.cache.page_log, max_q);
     if (p.nt) {
         if (a.cache.dim == 64) launch_attn_d<64>(a, p, dt, stream);
         else if (a.cache.dim == 128) launch_attn_d<128>(a, p, dt, stream);
         else launch_attn_d<256>(a, p, dt, stream);
     }
-    if (p.wr)
-        launch_kv_tiles(a, dt, p.wr, p.rows_max + 1, p.splits,
+    if (p.waves)
+        launch_kv_tiles(a, dt, p.waves, p.rows_max + 1, p.splits,
                         reinterpret_cast<float *>((char *)a.work + p.tile_parts), stream);
 }
 

@@ -3,11 +3,10 @@
 #pragma once
 
 #include "kv_device.h"
+#include "pipe_device.h"
 
 namespace sq {
 
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
@@ -39,6 +38,17 @@ __device__ __forceinline__ f32x16 mfma32(const uint4 &a, const uint4 &b, f32x16 
                                                       __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
+// A direct-to-LDS load of 4 bytes a lane (pipe_device.h), to lds_base + 4 lane.
+__device__ __forceinline__ void lds_dma4(const void *g, uint32_t lds_base) {
+    asm volatile(
+        "s_mov_b32 m0, %1\n\t"
+        "s_nop 0\n\t"
+        "global_load_lds_dword %0, off"
+        :
+        : "v"(g), "s"(lds_base)
+        : "memory", "m0");
+}
+
 // Two fp32 -> one word of the 16-bit type, to nearest even.
 template <int DT>
 __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
@@ -51,24 +61,11 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
     }
 }
 
-// The halves of a word that are infinite or NaN: as 1.0 of the type where the
-// value is +infinity or NaN (`up`), -infinity or NaN (`down`); the word with
-// those halves 0 is returned.
+// One half of a word of two 16-bit values, as fp32.
 template <int DT>
-__device__ __forceinline__ uint32_t split_nonfinite(uint32_t w, uint32_t &up, uint32_t &down) {
-    constexpr uint32_t kTop = DT == BF16 ? 0x7f80u : 0x7c00u, kOne = DT == BF16 ? 0x3f80u : 0x3c00u;
-    uint32_t keep = w;
-    up = down = 0;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const uint32_t x = (w >> (16 * h)) & 0xffffu, mag = x & 0x7fffu;
-        if (mag >= kTop) {
-            if (mag > kTop || x < 0x8000u) up |= kOne << (16 * h);
-            if (mag > kTop || x >= 0x8000u) down |= kOne << (16 * h);
-            keep &= ~(0xffffu << (16 * h));
-        }
-    }
-    return keep;
+__device__ __forceinline__ float half_of(uint32_t w, int h) {
+    if constexpr (DT == BF16) return __uint_as_float(h ? w & 0xffff0000u : w << 16);
+    else return (float)__builtin_bit_cast(f16x2, w)[h];
 }
 
 // Words that hold N bytes of codes, as loaded.
@@ -111,6 +108,20 @@ __device__ __forceinline__ uint32_t pair_of(const Words<N> &c, int q, float s) {
     } else {
         return q & 1 ? e4m3_pair<DT, true>(c.w[q >> 1], s) : e4m3_pair<DT, false>(c.w[q >> 1], s);
     }
+}
+
+// Whether a value of a block with this scale byte may be infinite or NaN in the
+// type (6 2^(e - 127) or 448 2^(e - 127) past its largest), or one of the codes
+// is a NaN (e4m3; the quantizer makes none).
+template <int FMT, int DT, int N>
+__device__ __forceinline__ bool may_be_nonfinite(const Words<N> &c, uint32_t e) {
+    constexpr uint32_t kFrom = DT == BF16 ? (FMT == E2M1 ? 253 : 247) : (FMT == E2M1 ? 141 : 135);
+    bool any = e >= kFrom;
+    if constexpr (FMT == E4M3) {
+#pragma unroll
+        for (int i = 0; i < (N + 3) / 4; ++i) any |= (((c.w[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0;
+    }
+    return any;
 }
 
 // One sequence's part in the call.  lo .. hi: the keys that any query sees.

@@ -3,32 +3,44 @@
 // of 32 x 32 x 16, and the keys and values of a tile converted once for a
 // block and shared through LDS.
 //
-// A block takes 128 WR rows (a row: a query of one of the heads that share the
-// key head), 32 WR a wave, over its keys in tiles of 64.  In LDS keys lie
+// A block takes 32 rows a wave (a row: a query of one of the heads that share
+// the key head) over its keys in tiles of 16 keys a wave.  In LDS keys lie
 // [key][channel], values [channel][key], both so that an operand is one
 // 16-byte read; the values' keys are in the order in which the weights lie in
 // the lanes.  Chunks of 16 bytes are exchanged by an xor with the row's number,
 // so that the lanes of a read take all banks.
+//
+// The matrix cores, LDS (a wave reads every key and value for its 32 rows) and
+// the softmax's vector instructions are about equally loaded, so a wave's loop
+// overlaps them: while the scores of the next 32 keys are multiplied the
+// weights of the last are formed, and while those multiply the values, the next
+// tile is converted into LDS and the next scores' maximum taken.  Keys and
+// values have two slots in LDS each, with two barriers a tile.
 #include "kv_attn_device.h"
 
 namespace sq {
 
-constexpr int kKeys = 64;
-
-// Where chunk `ch` (16 bytes) of key `key`, and of channel `d`, lies in LDS.
+// Where chunk `ch` (16 bytes) of key `key`, and of channel `d`, lies in a slot.
 template <int D>
 __device__ __forceinline__ int key_chunk(int key, int ch) { return key * (D / 8) + (ch ^ (key & 7)); }
-__device__ __forceinline__ int value_chunk(int d, int ch) { return d * (kKeys / 8) + (ch ^ ((d ^ d >> 3) & 7)); }
+template <int KT>
+__device__ __forceinline__ int value_chunk(int d, int ch) { return d * (KT / 8) + (ch ^ ((d ^ d >> 3) & 7)); }
 
-template <int D, int FMT, int DT, int WR>
-__global__ __launch_bounds__(256) void kv_tile_kernel(const KvAttention a, int rows_min, int splits, float *parts) {
-    constexpr int NB = D / 32, J = D / 16, S = D / 16, JT = D / 32, R = 128 * WR;
+template <int D, int FMT, int DT, int NW>
+__global__ __launch_bounds__(64 * NW, D < 256 ? 2 : 1) void kv_tile_kernel(const KvAttention a, int rows_min, int splits,
+                                                         float *parts, const int32_t *__restrict__ tables) {
+    constexpr int NB = D / 32, S = D / 16, JT = D / 32, R = 32 * NW;
+    constexpr int KT = 16 * NW, UNITS = KT / 32, NT = 64 * NW;  // keys of a tile, threads
     constexpr int RB = FMT == E2M1 ? D / 2 : D;
-    constexpr int KN = NB * (FMT == E2M1 ? 4 : 8);     // code bytes of a key, a quarter of its channels
-    constexpr int KS = NB < 4 ? 1 : NB / 4;            // scale bytes of those
-    constexpr int VN = FMT == E2M1 ? D / 32 : D / 16;  // code bytes of a value, a sixteenth of its channels
-    __shared__ uint4 s_k[kKeys * D / 8], s_v[kKeys * D / 8];
-    __shared__ int s_pre[257], s_at[2], s_bad[2];
+    // As a thread stages a tile: of one key a quarter of the channels, and of
+    // four successive keys a sixteenth of the values' channels.
+    constexpr int KN = RB / 4, KC = D / 4;     // code bytes and channels of a key
+    constexpr int KS = KC < 32 ? 1 : KC / 32;  // and scale bytes
+    constexpr int VN = RB / 16, VC = D / 16;
+    constexpr int SLOT = KT * D / 8;  // chunks of 16 bytes
+    __shared__ uint4 s_k[2 * SLOT], s_v[2 * SLOT];
+    __shared__ int s_pre[NT + 1], s_at[2];
+    __shared__ uint32_t s_apart[2][UNITS];
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -41,7 +53,7 @@ __global__ __launch_bounds__(256) void kv_tile_kernel(const KvAttention a, int r
         const int64_t rows = (int64_t)s.nq * group;
         return rows < rows_min ? 0 : (int)((rows + R - 1) / R);
     };
-    const int per_thread = (a.B + 255) / 256;
+    const int per_thread = (a.B + NT - 1) / NT;
     const int b_first = tid * per_thread;
     {
         int sum = 0;
@@ -49,14 +61,14 @@ __global__ __launch_bounds__(256) void kv_tile_kernel(const KvAttention a, int r
         s_pre[tid + 1] = sum;
         if (tid == 0) s_pre[0] = 0;
         __syncthreads();
-        for (int off = 1; off < 256; off <<= 1) {
+        for (int off = 1; off < NT; off <<= 1) {
             const int v = tid >= off ? s_pre[tid + 1 - off] : 0;
             __syncthreads();
             s_pre[tid + 1] += v;
             __syncthreads();
         }
     }
-    const int want = s_pre[256] - 1 - (int)(blockIdx.x / heads);
+    const int want = s_pre[NT] - 1 - (int)(blockIdx.x / heads);
     if (want < 0) return;
     if (s_pre[tid] <= want && want < s_pre[tid + 1]) {
         int before = s_pre[tid], b = b_first;
@@ -87,258 +99,283 @@ __global__ __launch_bounds__(256) void kv_tile_kernel(const KvAttention a, int r
     const int r_first = tile * R, r_end = r_first + R < rows ? r_first + R : rows;
     int t_all_lo, t_all_hi, t_lo, t_hi;
     span(r_first, r_end, t_all_lo, t_all_hi, t_lo, t_hi);
-    const int w_first = r_first + wave * 32 * WR;
-    const int w_end = w_first + 32 * WR < rows ? w_first + 32 * WR : rows;
+    const int w_first = r_first + wave * 32;
+    const int w_end = w_first + 32 < rows ? w_first + 32 : rows;
     int w_all_lo = 0, w_all_hi = 0, w_lo = 0, w_hi = 0;
     if (w_first < rows) span(w_first, w_end, w_all_lo, w_all_hi, w_lo, w_hi);
 
-    uint4 qf[WR][S];
-    int r_lo[WR], r_hi[WR];
+    uint4 qf[S];
+    const int row = w_first + n32;  // the lane's
+    const int query = row / group;
+    const char *const q_row = (const char *)a.q + ((int64_t)(seq.q0 + query) * a.q_st +
+                                                   (int64_t)(h * group + row - query * group) * a.q_sh) * 2;
 #pragma unroll
-    for (int wr = 0; wr < WR; ++wr) {
-        const int r = w_first + wr * 32 + n32;
-        const int i = r / group;
-        const char *x = (const char *)a.q +
-                        ((int64_t)(seq.q0 + i) * a.q_st + (int64_t)(h * group + r - i * group) * a.q_sh) * 2;
-#pragma unroll
-        for (int s = 0; s < S; ++s) {
-            qf[wr][s] = make_uint4(0, 0, 0, 0);
-            if (r < rows) qf[wr][s] = reinterpret_cast<const uint4 *>(x)[2 * s + hh];
+    for (int s = 0; s < S; ++s) {
+        qf[s] = make_uint4(0, 0, 0, 0);
+        if (row < rows) qf[s] = reinterpret_cast<const uint4 *>(q_row)[2 * s + hh];
+        if (a.scale < 0) {
+            qf[s].x ^= 0x80008000u;
+            qf[s].y ^= 0x80008000u;
+            qf[s].z ^= 0x80008000u;
+            qf[s].w ^= 0x80008000u;
         }
-        const int p = seq.nk - seq.nq + i;
-        r_hi[wr] = r < rows ? (a.causal ? p + 1 : seq.nk) : 0;
-        r_lo[wr] = a.window && (int64_t)p - a.window + 1 > 0 ? (int)(p - a.window + 1) : 0;
     }
+    const int place = seq.nk - seq.nq + query;
+    const int r_hi = row < rows ? (a.causal ? place + 1 : seq.nk) : 0;
+    const int r_lo = a.window && (int64_t)place - a.window + 1 > 0 ? (int)(place - a.window + 1) : 0;
 
-    float m[WR], l[WR];
-    f32x16 o[WR][JT];
+    float m = kNoMax, l = 0.0f;
+    f32x16 o[JT];
 #pragma unroll
-    for (int wr = 0; wr < WR; ++wr) {
-        m[wr] = kNoMax;
-        l[wr] = 0.0f;
+    for (int j = 0; j < JT; ++j)
 #pragma unroll
-        for (int j = 0; j < JT; ++j)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[wr][j][i] = 0.0f;
-    }
+        for (int i = 0; i < 16; ++i) o[j][i] = 0.0f;
 
     // The split's tiles of keys.
-    const int t_base = t_lo & ~(kKeys - 1);
-    const int n_tiles = t_hi > t_lo ? (t_hi - t_base + kKeys - 1) / kKeys : 0;
-    const int k0 = (int)((int64_t)n_tiles * split / splits), k1 = (int)((int64_t)n_tiles * (split + 1) / splits);
-    const float c = a.scale * 1.44269504088896341f;
-    const int32_t *const table = a.table + (int64_t)b * a.width;
+    const int t_base = t_lo & ~(KT - 1);
+    const int n_all = t_hi > t_lo ? (t_hi - t_base + KT - 1) / KT : 0;
+    const int k0 = (int)((int64_t)n_all * split / splits), k1 = (int)((int64_t)n_all * (split + 1) / splits);
+    const int n_tiles = k1 - k0;
+    // (a negative scale turns the queries; the maximum is taken before the scale)
+    const float c = fmaxf(fabsf(a.scale) * 1.44269504088896341f, 1e-37f);
+    const int32_t *const table = tables + (int64_t)b * a.width;
     const int g_last = (t_hi - 1) >> 4;
 
-    // As a thread stages a tile: a quarter of one key's channels, and of four
-    // successive keys a sixteenth of the values' channels.
+    // Loads of a tile into registers; tiles past the last are the last again.
     const int sk = tid >> 2, sc = tid & 3, sq4 = tid >> 4, sn = tid & 15;
     Words<KN> rk;
     uint32_t rks[KS];
     Words<VN> rv[4];
     uint32_t rvs[4];
-    const auto place = [&](int key, int64_t &row) -> bool {
-        int grp = key >> 4;
-        grp = grp < g_last ? grp : g_last;
-        int64_t page = table[grp >> (plog - 4)];
+    uint32_t nan_k, nan_v;  // 255 where the page is not in the cache
+    int page_k, page_v;     // of the next tile to load
+    const auto tile_at = [&](int i) { return t_base + (k0 + (i < n_tiles ? i : n_tiles - 1)) * KT; };
+    const auto group_of = [&](int key) { return key >> 4 < g_last ? key >> 4 : g_last; };
+    const auto page_of = [&](int key) { return table[group_of(key) >> (plog - 4)]; };
+    const auto row_of = [&](int key, int page, uint32_t &nan) -> int64_t {
         const bool held = page >= 0 && page < a.cache.pages;
-        page = held ? page : 0;
-        row = kv_row(a.cache, page, h, ((grp & ((1 << (plog - 4)) - 1)) << 4) + (key & 15));
-        return held;
+        nan = held ? 0u : 255u;
+        return kv_row(a.cache, held ? page : 0, h, ((group_of(key) & ((1 << (plog - 4)) - 1)) << 4) + (key & 15));
     };
-    const auto load = [&](int t) {
-        int64_t row;
-        bool held = place(t + sk, row);
+    const auto load_keys = [&](int i) {
+        const int64_t row = row_of(tile_at(i) + sk, page_k, nan_k);
         rk = load_codes<KN>(a.cache.kq + row * RB + sc * KN);
 #pragma unroll
-        for (int i = 0; i < KS; ++i) rks[i] = held ? a.cache.ks[row * NB + sc * NB / 4 + i] : 255u;
-        held = place(t + 4 * sq4, row);
+        for (int z = 0; z < KS; ++z) rks[z] = a.cache.ks[row * NB + sc * KC / 32 + z];
+        page_k = page_of(tile_at(i + 1) + sk);
+    };
+    const auto load_values = [&](int i) {
+        const int64_t row = row_of(tile_at(i) + 4 * sq4, page_v, nan_v);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            rv[i] = load_codes<VN>(a.cache.vq + (row + i) * RB + sn * VN);
-            rvs[i] = held ? a.cache.vs[(row + i) * NB + sn * NB / 16] : 255u;
+        for (int z = 0; z < 4; ++z) {
+            rv[z] = load_codes<VN>(a.cache.vq + (row + z) * RB + sn * VN);
+            rvs[z] = a.cache.vs[(row + z) * NB + sn * VC / 32];
+        }
+        page_v = page_of(tile_at(i + 1) + 4 * sq4);
+    };
+    const auto stage_keys = [&](int slot) {
+#pragma unroll
+        for (int z = 0; z < KC / 8; ++z) {
+            const float s = e8m0(rks[KC < 32 ? 0 : z / 4] | nan_k);
+            s_k[slot * SLOT + key_chunk<D>(sk, sc * (KC / 8) + z)] =
+                codes8_to_16<FMT, DT>(&rk.w[z * (FMT == E2M1 ? 1 : 2)], s);
         }
     };
-    const auto stage = [&](int t, int turn) {
+    const auto stage_values = [&](int i, int slot) {
+        const int t = tile_at(i);
 #pragma unroll
-        for (int i = 0; i < NB; ++i) {
-            const float s = e8m0(rks[NB < 4 ? 0 : i / 4]);
-            s_k[key_chunk<D>(sk, sc * NB + i)] =
-                codes8_to_16<FMT, DT>(&rk.w[i * (FMT == E2M1 ? 1 : 2)], s);
-        }
-        const bool masked = t < t_all_lo || t + kKeys > t_all_hi;
-        if (masked) {
-            // keys that no row of the block sees are taken as 0: what their
-            // place holds may be anything
+        for (int z = 0; z < 4; ++z) rvs[z] |= nan_v;
+        if (t < t_all_lo || t + KT > t_all_hi) {
+            asm volatile("");  // (a branch, not selects)
+            // Keys that no row of the block sees (behind the last, before the
+            // window) are taken as 0: what their place holds may be anything.
+            // Where an infinity or NaN may be, it is set apart: a weight of 0
+            // does not keep it from a row that must not see it.
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int key = t + 4 * sq4 + i;
-                if (key < t_lo || key >= t_hi) {
-                    rv[i] = Words<VN>{};
-                    rvs[i] = 0;
+            for (int z = 0; z < 4; ++z) {
+                const int key = 4 * sq4 + z;
+                const bool none = t + key < t_lo || t + key >= t_hi;
+                const bool alone = !none && may_be_nonfinite<FMT, DT>(rv[z], rvs[z]);
+                if (alone) atomicOr(&s_apart[slot][key >> 5], 1u << (key & 31));
+                if (none || alone) {
+                    rv[z] = Words<VN>{};
+                    rvs[z] = 0;
                 }
             }
         }
         // a quad of keys in its group of 16: quads 0, 2, 1, 3
         const int half = (sq4 & 3) >> 1, ch = (sq4 >> 2) * 2 + (sq4 & 1);
-        uint32_t bad = 0;
+        float s[4];
 #pragma unroll
-        for (int q = 0; q < J / 2; ++q) {
+        for (int z = 0; z < 4; ++z) s[z] = e8m0(rvs[z]);
+#pragma unroll
+        for (int q = 0; q < VC / 2; ++q) {
             uint32_t w[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = pair_of<FMT, DT>(rv[i], q, e8m0(rvs[i]));
-            if (masked) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t up, down;
-                    split_nonfinite<DT>(w[i], up, down);
-                    bad |= up | down;
-                }
-            }
+            for (int z = 0; z < 4; ++z) w[z] = pair_of<FMT, DT>(rv[z], q, s[z]);
 #pragma unroll
             for (int odd = 0; odd < 2; ++odd) {
                 const uint32_t sel = odd ? 0x07060302u : 0x05040100u;
-                reinterpret_cast<uint2 *>(s_v)[2 * value_chunk(sn * J + 2 * q + odd, ch) + half] =
+                reinterpret_cast<uint2 *>(s_v)[2 * (slot * SLOT + value_chunk<KT>(sn * VC + 2 * q + odd, ch)) + half] =
                     make_uint2(__builtin_amdgcn_perm(w[1], w[0], sel), __builtin_amdgcn_perm(w[3], w[2], sel));
             }
         }
-        if (bad) s_bad[turn] = 1;
     };
 
-    if (k0 < k1) load(t_base + k0 * kKeys);
-    if (tid == 0) s_bad[k0 & 1] = 0;
-    for (int k = k0; k < k1; ++k) {
-        const int t0 = t_base + k * kKeys;
-        __syncthreads();
-        stage(t0, k & 1);
-        if (tid == 0) s_bad[~k & 1] = 0;
-        __syncthreads();
-        const bool bad = __builtin_amdgcn_readfirstlane(s_bad[k & 1]) != 0;
-        if (k + 1 < k1) load(t0 + kKeys);
+    // Scores of 32 keys, their largest, the weights, the weighted values.
+    struct Weights { uint4 p[2]; };
+    const auto multiply_keys = [&](f32x16 &x, int slot, int sub) {
 #pragma unroll
-        for (int sub = 0; sub < 2; ++sub) {
-            const int t = t0 + 32 * sub;
-            if (t >= w_hi || t + 32 <= w_lo) continue;  // no row of the wave sees any
-            f32x16 st[WR];
+        for (int i = 0; i < 16; ++i) x[i] = 0.0f;
 #pragma unroll
-            for (int wr = 0; wr < WR; ++wr)
+        for (int s = 0; s < S; ++s)
+            x = mfma32<DT>(s_k[slot * SLOT + key_chunk<D>(32 * sub + n32, 2 * s + hh)], qf[s], x);
+    };
+    // The maximum that weights are taken against may trail the true one by 8
+    // (weights up to 256): rows are rescaled only where it is passed by more.
+    const auto take_maximum = [&](f32x16 &x, int t) {
+        if (t < w_all_lo || t + 32 > w_all_hi) {
+            asm volatile("");
 #pragma unroll
-                for (int i = 0; i < 16; ++i) st[wr][i] = 0.0f;
-#pragma unroll
-            for (int s = 0; s < S; ++s) {
-                const uint4 kf = s_k[key_chunk<D>(32 * sub + n32, 2 * s + hh)];
-#pragma unroll
-                for (int wr = 0; wr < WR; ++wr) st[wr] = mfma32<DT>(kf, qf[wr][s], st[wr]);
+            for (int i = 0; i < 16; ++i) {
+                const int key = t + (i & 3) + 8 * (i >> 2) + 4 * hh;
+                if (key < r_lo || key >= r_hi) x[i] = -INFINITY;
             }
-            const bool masked = t < w_all_lo || t + 32 > w_all_hi;
-            uint4 pf[WR][2], seen[WR][2];
+        }
+        float top = x[0];
 #pragma unroll
-            for (int wr = 0; wr < WR; ++wr) {
-                float top = -INFINITY;
+        for (int i = 1; i < 16; ++i) top = fmaxf(top, x[i]);
+        top *= c;
+        if (__any(top > m + 8.0f)) {
+            const float mn = fmaxf(m, fmaxf(top, __shfl_xor(top, 32, 64)));
+            const float f = __builtin_amdgcn_exp2f(m - mn);
+            m = mn;
+            l *= f;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) st[wr][i] *= c;
-                if (masked) {
-                    uint32_t v[8] = {};
+            for (int j = 0; j < JT; ++j) o[j] *= f;
+        }
+    };
+    const auto form_weights = [&](f32x16 &x, Weights &w) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int key = t + (i & 3) + 8 * (i >> 2) + 4 * hh;
-                        const bool vis = key >= r_lo[wr] && key < r_hi[wr];
-                        st[wr][i] = vis ? st[wr][i] : -INFINITY;
-                        v[i >> 1] |= vis ? (DT == BF16 ? 0x3f80u : 0x3c00u) << (16 * (i & 1)) : 0u;
-                    }
-                    seen[wr][0] = make_uint4(v[0], v[1], v[2], v[3]);
-                    seen[wr][1] = make_uint4(v[4], v[5], v[6], v[7]);
-                }
+        for (int i = 0; i < 16; ++i) {
+            x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], c, -m));
+            l += x[i];
+        }
 #pragma unroll
-                for (int i = 0; i < 16; ++i) top = fmaxf(top, st[wr][i]);
-                // (the maximum may trail by 8, as in kv_attn.hip)
-                if (__any(top > m[wr] + 8.0f)) {
-                    top = fmaxf(top, __shfl_xor(top, 32, 64));
-                    const float mn = fmaxf(m[wr], top);
-                    const float f = __builtin_amdgcn_exp2f(m[wr] - mn);
-                    m[wr] = mn;
-                    l[wr] *= f;
+        for (int u = 0; u < 2; ++u)
+            w.p[u] = make_uint4(pack16<DT>(x[8 * u], x[8 * u + 1]), pack16<DT>(x[8 * u + 2], x[8 * u + 3]),
+                                pack16<DT>(x[8 * u + 4], x[8 * u + 5]), pack16<DT>(x[8 * u + 6], x[8 * u + 7]));
+    };
+    const auto multiply_values = [&](const Weights &w, int slot, int sub) {
 #pragma unroll
-                    for (int j = 0; j < JT; ++j) o[wr][j] *= f;
-                }
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    st[wr][i] = __builtin_amdgcn_exp2f(st[wr][i] - m[wr]);
-                    l[wr] += st[wr][i];
-                }
+            for (int j = 0; j < JT; ++j)
+                o[j] = mfma32<DT>(s_v[slot * SLOT + value_chunk<KT>(32 * j + n32, 4 * sub + 2 * u + hh)], w.p[u], o[j]);
+    };
+    // (rare) The keys set apart, one at a time, for the rows that see them.
+    const auto add_apart = [&](const Weights &w, int t, uint32_t keys) {
+        for (; keys; keys &= keys - 1) {
+            const int n = __builtin_ctz(keys), key = t + n;
+            const int i = (n & 3) + 4 * (n >> 3), from = n32 + 32 * (n >> 2 & 1);
+            const int page = page_of(key);
+            const bool held = page >= 0 && page < a.cache.pages;
+            const int64_t at_row = kv_row(a.cache, held ? page : 0, h, key & ((1 << plog) - 1));
+            const uint32_t words[8] = {w.p[0].x, w.p[0].y, w.p[0].z, w.p[0].w, w.p[1].x, w.p[1].y, w.p[1].z, w.p[1].w};
+            uint32_t pair = words[0];
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
-                    pf[wr][u] = make_uint4(pack16<DT>(st[wr][8 * u], st[wr][8 * u + 1]),
-                                           pack16<DT>(st[wr][8 * u + 2], st[wr][8 * u + 3]),
-                                           pack16<DT>(st[wr][8 * u + 4], st[wr][8 * u + 5]),
-                                           pack16<DT>(st[wr][8 * u + 6], st[wr][8 * u + 7]));
-            }
+            for (int z = 1; z < 8; ++z) pair = z == i >> 1 ? words[z] : pair;
+            const float p = __shfl(half_of<DT>(pair, i & 1), from, 64);
 #pragma unroll
             for (int j = 0; j < JT; ++j)
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    uint4 vf = s_v[value_chunk(32 * j + n32, 4 * sub + 2 * u + hh)];
-                    if (bad) {
-                        // (as in kv_attn.hip: a weight of 0 would not keep them out)
-                        uint4 up, down;
-                        vf.x = split_nonfinite<DT>(vf.x, up.x, down.x);
-                        vf.y = split_nonfinite<DT>(vf.y, up.y, down.y);
-                        vf.z = split_nonfinite<DT>(vf.z, up.z, down.z);
-                        vf.w = split_nonfinite<DT>(vf.w, up.w, down.w);
+                for (int z = 0; z < 4; ++z) {  // channels d .. d + 3, of one staged part
+                    const int d = 32 * j + 8 * z + 4 * hh;
+                    const Words<VN> v = load_codes<VN>(a.cache.vq + at_row * RB + d / VC * VN);
+                    const uint32_t e = held ? a.cache.vs[at_row * NB + j] : 255u;
+                    if (!may_be_nonfinite<FMT, DT>(v, e)) continue;  // (not set apart)
 #pragma unroll
-                        for (int wr = 0; wr < WR; ++wr) {
-                            const uint32_t one = DT == BF16 ? 0x3f803f80u : 0x3c003c00u;
-                            const uint4 see = masked ? seen[wr][u] : make_uint4(one, one, one, one);
-                            f32x16 z;
+                    for (int y = 0; y < 4; ++y) {
+                        float val = 0.0f;
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) z[i] = 0.0f;
-                            const f32x16 cu = mfma32<DT>(up, see, z);
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                if (cu[i] > 0) o[wr][j][i] += INFINITY;
-                            const f32x16 cd = mfma32<DT>(down, see, z);
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                if (cd[i] > 0) o[wr][j][i] -= INFINITY;
-                        }
+                        for (int at = 0; at < VC; at += 4)
+                            if (d % VC == at) val = half_of<DT>(pair_of<FMT, DT>(v, (at + y) >> 1, e8m0(e)), y & 1);
+                        if (key >= r_lo && key < r_hi) o[j][4 * z + y] += p * val;
                     }
-#pragma unroll
-                    for (int wr = 0; wr < WR; ++wr) o[wr][j] = mfma32<DT>(vf, pf[wr][u], o[wr][j]);
                 }
+        }
+    };
+
+    if (tid < 2 * UNITS) s_apart[tid / UNITS][tid % UNITS] = 0;
+    if (n_tiles > 0) {
+        page_k = page_of(tile_at(0) + sk);
+        page_v = page_of(tile_at(0) + 4 * sq4);
+        load_keys(0);
+        load_values(0);
+        __syncthreads();  // (s_apart)
+        stage_keys(0);
+        stage_values(0, 0);
+        load_keys(1);
+        load_values(1);
+        __syncthreads();
+        f32x16 x[2];
+        Weights w;
+        multiply_keys(x[0], 0, 0);
+        take_maximum(x[0], tile_at(0));
+        for (int i = 0; i < n_tiles; ++i) {
+            const int t = tile_at(i), slot = i & 1;
+#pragma unroll
+            for (int u = 0; u < UNITS; ++u) {
+                // unit u is weighted, the next one scored
+                const bool last = u == UNITS - 1;
+                multiply_keys(x[~u & 1], last ? slot ^ 1 : slot, last ? 0 : u + 1);
+                form_weights(x[u & 1], w);
+                multiply_values(w, slot, u);
+                if (u == 0) {
+                    stage_keys(slot ^ 1);
+                    load_keys(i + 2);
+                    if (tid < UNITS) s_apart[slot ^ 1][tid] = 0;
+                }
+                if (last) {
+                    stage_values(i + 1, slot ^ 1);
+                    load_values(i + 2);
+                }
+                const uint32_t apart = __builtin_amdgcn_readfirstlane(s_apart[slot][u]);
+                if (apart) add_apart(w, t + 32 * u, apart);
+                take_maximum(x[~u & 1], last ? tile_at(i + 1) : t + 32 * (u + 1));
+                // the next tile's keys are read from the last unit on, its values
+                // from the first of the next
+                if (u >= UNITS - 2) __syncthreads();
+            }
         }
     }
 
+    l += __shfl_xor(l, 32, 64);
+    if (row >= rows) return;
+    const int64_t out = (int64_t)(seq.q0 + query) * a.q_heads + h * group + row - query * group;
+    if (splits == 1) {
+        const float inv = row_factor(l, seq.over);
+        uint2 *y = reinterpret_cast<uint2 *>(a.y) + out * (D / 4) + hh;
 #pragma unroll
-    for (int wr = 0; wr < WR; ++wr) {
-        const int r = w_first + wr * 32 + n32;
-        l[wr] += __shfl_xor(l[wr], 32, 64);
-        if (r >= rows) continue;
-        const int i = r / group;
-        const int64_t row = (int64_t)(seq.q0 + i) * a.q_heads + h * group + r - i * group;
-        if (splits == 1) {
-            const float inv = row_factor(l[wr], seq.over);
-            uint2 *y = reinterpret_cast<uint2 *>(a.y) + row * (D / 4) + hh;
+        for (int j = 0; j < JT; ++j)
 #pragma unroll
-            for (int j = 0; j < JT; ++j)
+            for (int k = 0; k < 4; ++k)
+                y[8 * j + 2 * k] = make_uint2(pack16<DT>(o[j][4 * k] * inv, o[j][4 * k + 1] * inv),
+                                              pack16<DT>(o[j][4 * k + 2] * inv, o[j][4 * k + 3] * inv));
+    } else {
+        // values of all rows and splits, then their maxima and sums
+        const int64_t all = (int64_t)a.T * a.q_heads;
+        float *y = parts + (split * all + out) * D + 4 * hh;
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    y[8 * j + 2 * k] = make_uint2(pack16<DT>(o[wr][j][4 * k] * inv, o[wr][j][4 * k + 1] * inv),
-                                                  pack16<DT>(o[wr][j][4 * k + 2] * inv, o[wr][j][4 * k + 3] * inv));
-        } else {
-            // values of all rows and splits, then their maxima and sums
-            const int64_t all = (int64_t)a.T * a.q_heads;
-            float *y = parts + (split * all + row) * D + 4 * hh;
+        for (int j = 0; j < JT; ++j)
 #pragma unroll
-            for (int j = 0; j < JT; ++j)
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    *reinterpret_cast<float4 *>(y + 32 * j + 8 * k) =
-                        make_float4(o[wr][j][4 * k], o[wr][j][4 * k + 1], o[wr][j][4 * k + 2], o[wr][j][4 * k + 3]);
-            if (hh == 0) {
-                float *s = parts + splits * all * D + (split * all + row) * 2;
-                s[0] = m[wr];
-                s[1] = l[wr];
-            }
+            for (int k = 0; k < 4; ++k)
+                *reinterpret_cast<float4 *>(y + 32 * j + 8 * k) =
+                    make_float4(o[j][4 * k], o[j][4 * k + 1], o[j][4 * k + 2], o[j][4 * k + 3]);
+        if (hh == 0) {
+            float *s = parts + splits * all * D + (split * all + out) * 2;
+            s[0] = m;
+            s[1] = l;
         }
     }
 }
@@ -371,10 +408,11 @@ __global__ __launch_bounds__(256) void kv_tile_join_kernel(const KvAttention a, 
         make_uint2(pack16<DT>(v[0] * inv, v[1] * inv), pack16<DT>(v[2] * inv, v[3] * inv));
 }
 
-template <int D, int FMT, int DT, int WR>
+template <int D, int FMT, int DT, int NW>
 static void launch_tile(const KvAttention &a, int rows_min, int splits, float *parts, hipStream_t stream) {
-    const int64_t tiles = a.T * a.group / (128 * WR) + (a.B < a.T ? a.B : a.T);
-    kv_tile_kernel<D, FMT, DT, WR><<<dim3((unsigned)(tiles * a.cache.heads), splits), 256, 0, stream>>>(a, rows_min, splits, parts);
+    const int64_t tiles = a.T * a.group / (32 * NW) + (a.B < a.T ? a.B : a.T);
+    kv_tile_kernel<D, FMT, DT, NW><<<dim3((unsigned)(tiles * a.cache.heads), splits), 64 * NW, 0, stream>>>(
+        a, rows_min, splits, parts, a.table);
     if (splits > 1) {
         const int64_t rows = a.T * a.q_heads, per = 256 / (D / 4);
         kv_tile_join_kernel<D, DT><<<(unsigned)((rows + per - 1) / per), 256, 0, stream>>>(a, rows_min, splits, parts);
@@ -382,30 +420,31 @@ static void launch_tile(const KvAttention &a, int rows_min, int splits, float *p
 }
 
 template <int D, int FMT, int DT>
-static void launch_tile_wr(const KvAttention &a, int wr, int rows_min, int splits, float *parts, hipStream_t stream) {
+static void launch_tile_nw(const KvAttention &a, int waves, int rows_min, int splits, float *parts,
+                           hipStream_t stream) {
     if constexpr (D < 256) {
-        if (wr == 2) return launch_tile<D, FMT, DT, 2>(a, rows_min, splits, parts, stream);
+        if (waves == 8) return launch_tile<D, FMT, DT, 8>(a, rows_min, splits, parts, stream);
     }
-    launch_tile<D, FMT, DT, 1>(a, rows_min, splits, parts, stream);
+    launch_tile<D, FMT, DT, 4>(a, rows_min, splits, parts, stream);
 }
 
 template <int D>
-static void launch_tile_d(const KvAttention &a, int dt, int wr, int rows_min, int splits, float *parts,
+static void launch_tile_d(const KvAttention &a, int dt, int waves, int rows_min, int splits, float *parts,
                           hipStream_t stream) {
     if (a.cache.fmt == E2M1) {
-        if (dt == F16) launch_tile_wr<D, E2M1, F16>(a, wr, rows_min, splits, parts, stream);
-        else launch_tile_wr<D, E2M1, BF16>(a, wr, rows_min, splits, parts, stream);
+        if (dt == F16) launch_tile_nw<D, E2M1, F16>(a, waves, rows_min, splits, parts, stream);
+        else launch_tile_nw<D, E2M1, BF16>(a, waves, rows_min, splits, parts, stream);
     } else {
-        if (dt == F16) launch_tile_wr<D, E4M3, F16>(a, wr, rows_min, splits, parts, stream);
-        else launch_tile_wr<D, E4M3, BF16>(a, wr, rows_min, splits, parts, stream);
+        if (dt == F16) launch_tile_nw<D, E4M3, F16>(a, waves, rows_min, splits, parts, stream);
+        else launch_tile_nw<D, E4M3, BF16>(a, waves, rows_min, splits, parts, stream);
     }
 }
 
-void launch_kv_tiles(const KvAttention &a, int dt, int wr, int rows_min, int splits, float *parts,
+void launch_kv_tiles(const KvAttention &a, int dt, int waves, int rows_min, int splits, float *parts,
                      hipStream_t stream) {
-    if (a.cache.dim == 64) launch_tile_d<64>(a, dt, wr, rows_min, splits, parts, stream);
-    else if (a.cache.dim == 128) launch_tile_d<128>(a, dt, wr, rows_min, splits, parts, stream);
-    else launch_tile_d<256>(a, dt, wr, rows_min, splits, parts, stream);
+    if (a.cache.dim == 64) launch_tile_d<64>(a, dt, waves, rows_min, splits, parts, stream);
+    else if (a.cache.dim == 128) launch_tile_d<128>(a, dt, waves, rows_min, splits, parts, stream);
+    else launch_tile_d<256>(a, dt, waves, rows_min, splits, parts, stream);
 }
 
 }  // namespace sq

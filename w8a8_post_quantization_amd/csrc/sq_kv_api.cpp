@@ -154,7 +154,7 @@ size_t sq_attention_kv_mx_workspace(int64_t T, int64_t q_heads, const sq_kv_cach
     sq::KvCache c;
     if (check_cache(cache, c) || check_attention(T, q_heads, c, B, width, max_q)) return 0;
     if (T == 0 || B == 0) return 0;
-    return sq::kv_attention_workspace(T, (int)q_heads, c.heads, c.dim, (int)B, width << c.page_log,
+    return sq::kv_attention_workspace(T, (int)q_heads, c.heads, c.dim, c.fmt, (int)B, width << c.page_log,
                                       most_queries(max_q, T));
 }
 
@@ -177,7 +177,7 @@ int sq_attention_kv_mx(const void *q, const int64_t q_stride[2], int dt, int64_t
     if (!seq_lens || !y || (width && !table)) return SQ_ERR_NULL;
     if (!aligned(y, 16) || !aligned(table, 4) || !aligned(seq_lens, 4) || !aligned(cu_q, 4)) return SQ_ERR_ALIGN;
     const int64_t most = cu_q ? most_queries(max_q, T) : 1;
-    const size_t need = sq::kv_attention_workspace(T, (int)q_heads, a.cache.heads, a.cache.dim, (int)B,
+    const size_t need = sq::kv_attention_workspace(T, (int)q_heads, a.cache.heads, a.cache.dim, a.cache.fmt, (int)B,
                                                    width << a.cache.page_log, most);
     if (!workspace || workspace_bytes < need) return SQ_ERR_WORKSPACE;
     if (!aligned(workspace, 16)) return SQ_ERR_ALIGN;

@@ -58,11 +58,11 @@ struct KvAttention {
     int64_t window;  // 0: none
     void *work;
 };
-size_t kv_attention_workspace(int64_t T, int q_heads, int heads, int dim, int B, int64_t keys,
+size_t kv_attention_workspace(int64_t T, int q_heads, int heads, int dim, int fmt, int B, int64_t keys,
                               int64_t max_q);
-// The tile kernel: sequences of rows_min rows and more, wr row groups a wave,
+// The tile kernel: sequences of rows_min rows and more, 4 or 8 waves a block,
 // the keys in so many splits (their parts, where there are several, in `parts`).
-void launch_kv_tiles(const KvAttention &a, int dt, int wr, int rows_min, int splits, float *parts,
+void launch_kv_tiles(const KvAttention &a, int dt, int waves, int rows_min, int splits, float *parts,
                      hipStream_t stream);
 void launch_kv_attention(const KvAttention &a, int64_t max_q, int dt, hipStream_t stream);
 
