@@ -82,7 +82,7 @@ __global__ __launch_bounds__(256, (blocks_per_cu(D, FMT, NT))) void kv_attn_kern
     Part *const part = reinterpret_cast<Part *>(work);
     float *const parts = work + kMaxBlocks * sizeof(Part) / sizeof(float);
 
-    const auto units_of = [&](const KvSeq &s) -> int {
+    const auto units_of = [&](const KvSeq &s) SQ_INLINE -> int {
         if (s.nq == 0 || (int64_t)s.nq * group > rows_max || s.hi <= s.lo) return 0;
         return (s.hi - (s.lo & ~15) + kTile - 1) / kTile;
     };
@@ -190,14 +190,14 @@ __global__ __launch_bounds__(256, (blocks_per_cu(D, FMT, NT))) void kv_attn_kern
         // the cache is kept as two bits a tile, the newest lowest.
         int page[2];
         uint32_t missing = 0;
-        const auto look_up = [&](int t) {
+        const auto look_up = [&](int t) SQ_INLINE {
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 const int grp = (t >> 4) + half;
                 page[half] = table[__builtin_amdgcn_readfirstlane(grp < g_last ? grp : g_last) >> (plog - 4)];
             }
         };
-        const auto load = [&](int t, int slot) {
+        const auto load = [&](int t, int slot) SQ_INLINE {
             int64_t row[2];
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
@@ -230,7 +230,7 @@ __global__ __launch_bounds__(256, (blocks_per_cu(D, FMT, NT))) void kv_attn_kern
                 lds_dma4(e + (w % W < W / 2 ? row[0] : row[1]) * NB + w % (W / 2) * 4, to + 2 * L::codes + i * 256);
             }
         };
-        const auto compute = [&](int t, int slot, uint32_t gone) {
+        const auto compute = [&](int t, int slot, uint32_t gone) SQ_INLINE {
             const bool masked = t < all_lo || t + 32 > all_hi || t + 32 > te;
             const uint8_t *const kq = ring + slot * L::bytes, *const vq = kq + L::codes;
             const uint8_t *const ks = vq + L::codes, *const vs = ks + L::scales;
@@ -519,8 +519,8 @@ __global__ __launch_bounds__(256) void kv_join_kernel(const KvAttention a) {
     const int d4 = threadIdx.x % Q, w = threadIdx.x / Q;
     const int first = blockIdx.x, n = p.last - first + 1;
     // (the first block's part is its second: it begins the item)
-    const auto part = [&](int i) { return parts + (int64_t)((first + i) * 2 + (i == 0)) * PartSize<D, NT>::floats; };
-    const auto reduced = [&](float v, auto op) {
+    const auto part = [&](int i) SQ_INLINE { return parts + (int64_t)((first + i) * 2 + (i == 0)) * PartSize<D, NT>::floats; };
+    const auto reduced = [&](float v, auto op) SQ_INLINE {
 #pragma unroll
         for (int off = 32; off; off >>= 1) v = op(v, __shfl_xor(v, off, 64));
         if ((threadIdx.x & 63) == 0) s_red[threadIdx.x >> 6] = v;

@@ -7,6 +7,9 @@
 
 namespace sq {
 
+// For a kernel's lambdas: left as calls, they would have its registers in memory.
+#define SQ_INLINE __attribute__((always_inline))
+
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 

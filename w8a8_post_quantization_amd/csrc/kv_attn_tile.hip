@@ -4,33 +4,58 @@
 // block and shared through LDS.
 //
 // A block takes 32 rows a wave (a row: a query of one of the heads that share
-// the key head) over its keys in tiles of 16 keys a wave.  In LDS keys lie
-// [key][channel], values [channel][key], both so that an operand is one
-// 16-byte read; the values' keys are in the order in which the weights lie in
-// the lanes.  Chunks of 16 bytes are exchanged by an xor with the row's number,
-// so that the lanes of a read take all banks.
+// the key head) over its keys in tiles of 128 (64 with 256 channels).  In LDS
+// keys lie [key][channel], values [channel][key], both so that an operand is
+// one 16-byte read; the values' keys are in the order in which the weights lie
+// in the lanes.  Chunks of 16 bytes are exchanged by an xor with the row's
+// number, so that the lanes of a read take all banks.
 //
 // The matrix cores, LDS (a wave reads every key and value for its 32 rows) and
 // the softmax's vector instructions are about equally loaded, so a wave's loop
-// overlaps them: while the scores of the next 32 keys are multiplied the
-// weights of the last are formed, and while those multiply the values, the next
-// tile is converted into LDS and the next scores' maximum taken.  Keys and
-// values have two slots in LDS each, with two barriers a tile.
+// overlaps them.  It goes in units of 32 keys: while the scores of the next
+// unit are multiplied the weights of this one are formed; while those multiply
+// the values, a part of the next tile is converted into LDS and the next
+// scores' maximum is taken.  Operands are read from LDS half a unit ahead.  Keys
+// and values have two slots in LDS each, with two barriers a tile.
+#include <type_traits>
+
 #include "kv_attn_device.h"
 
 namespace sq {
 
-// Where chunk `ch` (16 bytes) of key `key`, and of channel `d`, lies in a slot.
+// Where chunk `ch` (16 bytes) of key `key`, and of channel `d`, lies in a slot
+// (of KT keys).  LDS moves 256 bytes a clock, 16 lanes of a read: rows of 256
+// bytes and more exchange their chunks 16 ways, rows of 128 bytes lie in pairs
+// and exchange 8 ways.  Staging writes one channel in D / 16 at a time, so the
+// values' exchange takes the higher bits of the channel, too.
 template <int D>
-__device__ __forceinline__ int key_chunk(int key, int ch) { return key * (D / 8) + (ch ^ (key & 7)); }
-template <int KT>
-__device__ __forceinline__ int value_chunk(int d, int ch) { return d * (KT / 8) + (ch ^ ((d ^ d >> 3) & 7)); }
+__device__ __forceinline__ int key_chunk(int key, int ch) {
+    return key * (D / 8) + (ch ^ (D == 64 ? key >> 1 & 7 : key & 15));
+}
+template <int D>
+__device__ __forceinline__ int value_exchange(int d) {
+    return D == 64 ? (d ^ d >> 2) & 15 : D == 128 ? (d ^ d >> 3) & 15 : (d >> 1 ^ d >> 4) & 7;
+}
+template <int D, int KT>
+__device__ __forceinline__ int value_chunk(int d, int ch) { return d * (KT / 8) + (ch ^ value_exchange<D>(d)); }
+
+// The order of what follows the last scheduling barrier: a matrix instruction,
+// N vector instructions, R times.
+template <int R, int N>
+__device__ __forceinline__ void mfma_with() {
+    if constexpr (R > 0) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, N, 0);
+        mfma_with<R - 1, N>();
+    }
+}
 
 template <int D, int FMT, int DT, int NW>
 __global__ __launch_bounds__(64 * NW, D < 256 ? 2 : 1) void kv_tile_kernel(const KvAttention a, int rows_min, int splits,
                                                          float *parts, const int32_t *__restrict__ tables) {
     constexpr int NB = D / 32, S = D / 16, JT = D / 32, R = 32 * NW;
-    constexpr int KT = 16 * NW, UNITS = KT / 32, NT = 64 * NW;  // keys of a tile, threads
+    constexpr int KT = D < 256 ? 128 : 64, UNITS = KT / 32, NT = 64 * NW;  // keys, units of a tile; threads
+    constexpr int PASS = 4 * KT / NT;  // times that a thread stages
     constexpr int RB = FMT == E2M1 ? D / 2 : D;
     // As a thread stages a tile: of one key a quarter of the channels, and of
     // four successive keys a sixteenth of the values' channels.
@@ -38,7 +63,8 @@ __global__ __launch_bounds__(64 * NW, D < 256 ? 2 : 1) void kv_tile_kernel(const
     constexpr int KS = KC < 32 ? 1 : KC / 32;  // and scale bytes
     constexpr int VN = RB / 16, VC = D / 16;
     constexpr int SLOT = KT * D / 8;  // chunks of 16 bytes
-    __shared__ uint4 s_k[2 * SLOT], s_v[2 * SLOT];
+    __shared__ __attribute__((aligned(1024))) uint4 s_kv[4 * SLOT];
+    uint4 *const s_k = s_kv, *const s_v = s_kv + 2 * SLOT;
     __shared__ int s_pre[NT + 1], s_at[2];
     __shared__ uint32_t s_apart[2][UNITS];
 
@@ -49,7 +75,7 @@ __global__ __launch_bounds__(64 * NW, D < 256 ? 2 : 1) void kv_tile_kernel(const
 
     // The block's rows: tiles of all long sequences in a row, the last (with the
     // most keys) first.
-    const auto tiles_of = [&](const KvSeq &s) -> int {
+    const auto tiles_of = [&](const KvSeq &s) SQ_INLINE -> int {
         const int64_t rows = (int64_t)s.nq * group;
         return rows < rows_min ? 0 : (int)((rows + R - 1) / R);
     };
@@ -89,7 +115,7 @@ __global__ __launch_bounds__(64 * NW, D < 256 ? 2 : 1) void kv_tile_kernel(const
     const int rows = seq.nq * group;  // (T * q_heads < 2^31)
 
     // Keys that the rows from r to e - 1 see: all of them, any of them.
-    const auto span = [&](int r, int e, int &all_lo, int &all_hi, int &any_lo, int &any_hi) {
+    const auto span = [&](int r, int e, int &all_lo, int &all_hi, int &any_lo, int &any_hi) SQ_INLINE {
         const int p0 = seq.nk - seq.nq + r / group, p1 = seq.nk - seq.nq + (e - 1) / group;
         any_hi = a.causal ? (p1 + 1 > 0 ? p1 + 1 : 0) : seq.nk;
         all_hi = a.causal ? p0 + 1 : seq.nk;
@@ -142,110 +168,158 @@ __global__ __launch_bounds__(64 * NW, D < 256 ? 2 : 1) void kv_tile_kernel(const
     const int g_last = (t_hi - 1) >> 4;
 
     // Loads of a tile into registers; tiles past the last are the last again.
+    // (pass p of a thread: key sk + p NT / 4, keys 4 (sq4 + p NT / 16) ..)
     const int sk = tid >> 2, sc = tid & 3, sq4 = tid >> 4, sn = tid & 15;
-    Words<KN> rk;
-    uint32_t rks[KS];
-    Words<VN> rv[4];
-    uint32_t rvs[4];
-    uint32_t nan_k, nan_v;  // 255 where the page is not in the cache
-    int page_k, page_v;     // of the next tile to load
-    const auto tile_at = [&](int i) { return t_base + (k0 + (i < n_tiles ? i : n_tiles - 1)) * KT; };
-    const auto group_of = [&](int key) { return key >> 4 < g_last ? key >> 4 : g_last; };
-    const auto page_of = [&](int key) { return table[group_of(key) >> (plog - 4)]; };
-    const auto row_of = [&](int key, int page, uint32_t &nan) -> int64_t {
+    Words<KN> rk[PASS];
+    uint32_t rks[PASS][KS];
+    Words<VN> rv[PASS][4];
+    uint32_t rvs[PASS][4];
+    uint32_t nan_k[PASS], nan_v[PASS];  // 255 where the page is not in the cache
+    int page_k[PASS], page_v[PASS];     // of the next tile to load
+    const auto tile_at = [&](int i) SQ_INLINE { return t_base + (k0 + (i < n_tiles ? i : n_tiles - 1)) * KT; };
+    const auto group_of = [&](int key) SQ_INLINE { return key >> 4 < g_last ? key >> 4 : g_last; };
+    const auto page_of = [&](int key) SQ_INLINE { return table[group_of(key) >> (plog - 4)]; };
+    const auto row_of = [&](int key, int page, uint32_t &nan) SQ_INLINE -> int64_t {
         const bool held = page >= 0 && page < a.cache.pages;
         nan = held ? 0u : 255u;
         return kv_row(a.cache, held ? page : 0, h, ((group_of(key) & ((1 << (plog - 4)) - 1)) << 4) + (key & 15));
     };
-    const auto load_keys = [&](int i) {
-        const int64_t row = row_of(tile_at(i) + sk, page_k, nan_k);
-        rk = load_codes<KN>(a.cache.kq + row * RB + sc * KN);
+    const auto look_up_keys = [&](int i) SQ_INLINE {
 #pragma unroll
-        for (int z = 0; z < KS; ++z) rks[z] = a.cache.ks[row * NB + sc * KC / 32 + z];
-        page_k = page_of(tile_at(i + 1) + sk);
+        for (int p = 0; p < PASS; ++p) page_k[p] = page_of(tile_at(i) + sk + p * (NT / 4));
     };
-    const auto load_values = [&](int i) {
-        const int64_t row = row_of(tile_at(i) + 4 * sq4, page_v, nan_v);
+    const auto look_up_values = [&](int i) SQ_INLINE {
 #pragma unroll
-        for (int z = 0; z < 4; ++z) {
-            rv[z] = load_codes<VN>(a.cache.vq + (row + z) * RB + sn * VN);
-            rvs[z] = a.cache.vs[(row + z) * NB + sn * VC / 32];
+        for (int p = 0; p < PASS; ++p) page_v[p] = page_of(tile_at(i) + 4 * (sq4 + p * (NT / 16)));
+    };
+    const auto load_keys = [&](int i) SQ_INLINE {
+#pragma unroll
+        for (int p = 0; p < PASS; ++p) {
+            const int64_t at = row_of(tile_at(i) + sk + p * (NT / 4), page_k[p], nan_k[p]);
+            rk[p] = load_codes<KN>(a.cache.kq + at * RB + sc * KN);
+#pragma unroll
+            for (int z = 0; z < KS; ++z) rks[p][z] = a.cache.ks[at * NB + sc * KC / 32 + z];
         }
-        page_v = page_of(tile_at(i + 1) + 4 * sq4);
+        look_up_keys(i + 1);
     };
-    const auto stage_keys = [&](int slot) {
+    const auto load_values = [&](int i) SQ_INLINE {
 #pragma unroll
-        for (int z = 0; z < KC / 8; ++z) {
-            const float s = e8m0(rks[KC < 32 ? 0 : z / 4] | nan_k);
-            s_k[slot * SLOT + key_chunk<D>(sk, sc * (KC / 8) + z)] =
-                codes8_to_16<FMT, DT>(&rk.w[z * (FMT == E2M1 ? 1 : 2)], s);
-        }
-    };
-    const auto stage_values = [&](int i, int slot) {
-        const int t = tile_at(i);
-#pragma unroll
-        for (int z = 0; z < 4; ++z) rvs[z] |= nan_v;
-        if (t < t_all_lo || t + KT > t_all_hi) {
-            asm volatile("");  // (a branch, not selects)
-            // Keys that no row of the block sees (behind the last, before the
-            // window) are taken as 0: what their place holds may be anything.
-            // Where an infinity or NaN may be, it is set apart: a weight of 0
-            // does not keep it from a row that must not see it.
+        for (int p = 0; p < PASS; ++p) {
+            const int64_t at = row_of(tile_at(i) + 4 * (sq4 + p * (NT / 16)), page_v[p], nan_v[p]);
 #pragma unroll
             for (int z = 0; z < 4; ++z) {
-                const int key = 4 * sq4 + z;
-                const bool none = t + key < t_lo || t + key >= t_hi;
-                const bool alone = !none && may_be_nonfinite<FMT, DT>(rv[z], rvs[z]);
-                if (alone) atomicOr(&s_apart[slot][key >> 5], 1u << (key & 31));
-                if (none || alone) {
-                    rv[z] = Words<VN>{};
-                    rvs[z] = 0;
-                }
+                rv[p][z] = load_codes<VN>(a.cache.vq + (at + z) * RB + sn * VN);
+                rvs[p][z] = a.cache.vs[(at + z) * NB + sn * VC / 32];
             }
         }
-        // a quad of keys in its group of 16: quads 0, 2, 1, 3
-        const int half = (sq4 & 3) >> 1, ch = (sq4 >> 2) * 2 + (sq4 & 1);
-        float s[4];
+        look_up_values(i + 1);
+    };
+    const auto stage_keys = [&](int slot) SQ_INLINE {
 #pragma unroll
-        for (int z = 0; z < 4; ++z) s[z] = e8m0(rvs[z]);
+        for (int p = 0; p < PASS; ++p)
 #pragma unroll
-        for (int q = 0; q < VC / 2; ++q) {
-            uint32_t w[4];
+            for (int z = 0; z < KC / 8; ++z) {
+                const float s = e8m0(rks[p][KC < 32 ? 0 : z / 4] | nan_k[p]);
+                s_k[slot * SLOT + key_chunk<D>(sk + p * (NT / 4), sc * (KC / 8) + z)] =
+                    codes8_to_16<FMT, DT>(&rk[p].w[z * (FMT == E2M1 ? 1 : 2)], s);
+            }
+    };
+    const auto stage_values = [&](int i, int slot) SQ_INLINE {
+        const int t = tile_at(i);
 #pragma unroll
-            for (int z = 0; z < 4; ++z) w[z] = pair_of<FMT, DT>(rv[z], q, s[z]);
+        for (int p = 0; p < PASS; ++p) {
+            const int quad = sq4 + p * (NT / 16);
 #pragma unroll
-            for (int odd = 0; odd < 2; ++odd) {
-                const uint32_t sel = odd ? 0x07060302u : 0x05040100u;
-                reinterpret_cast<uint2 *>(s_v)[2 * (slot * SLOT + value_chunk<KT>(sn * VC + 2 * q + odd, ch)) + half] =
-                    make_uint2(__builtin_amdgcn_perm(w[1], w[0], sel), __builtin_amdgcn_perm(w[3], w[2], sel));
+            for (int z = 0; z < 4; ++z) rvs[p][z] |= nan_v[p];
+            if (t < t_all_lo || t + KT > t_all_hi) {
+                asm volatile("");  // (a branch, not selects)
+                // Keys that no row of the block sees (behind the last, before the
+                // window) are taken as 0: what their place holds may be anything.
+                // Where an infinity or NaN may be, it is set apart: a weight of 0
+                // does not keep it from a row that must not see it.
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                    const int key = 4 * quad + z;
+                    const bool none = t + key < t_lo || t + key >= t_hi;
+                    const bool alone = !none && may_be_nonfinite<FMT, DT>(rv[p][z], rvs[p][z]);
+                    if (alone) atomicOr(&s_apart[slot][key >> 5], 1u << (key & 31));
+                    if (none || alone) {
+                        rv[p][z] = Words<VN>{};
+                        rvs[p][z] = 0;
+                    }
+                }
+            }
+            // a quad of keys in its group of 16: quads 0, 2, 1, 3
+            const int half = (quad & 3) >> 1, ch = (quad >> 2) * 2 + (quad & 1);
+            float s[4];
+#pragma unroll
+            for (int z = 0; z < 4; ++z) s[z] = e8m0(rvs[p][z]);
+#pragma unroll
+            for (int q = 0; q < VC / 2; ++q) {
+                uint32_t w[4];
+#pragma unroll
+                for (int z = 0; z < 4; ++z) w[z] = pair_of<FMT, DT>(rv[p][z], q, s[z]);
+#pragma unroll
+                for (int odd = 0; odd < 2; ++odd) {
+                    const uint32_t sel = odd ? 0x07060302u : 0x05040100u;
+                    reinterpret_cast<uint2 *>(s_v)[2 * (slot * SLOT + value_chunk<D, KT>(sn * VC + 2 * q + odd, ch)) + half] =
+                        make_uint2(__builtin_amdgcn_perm(w[1], w[0], sel), __builtin_amdgcn_perm(w[3], w[2], sel));
+                }
             }
         }
     };
 
     // Scores of 32 keys, their largest, the weights, the weighted values.
     struct Weights { uint4 p[2]; };
-    const auto multiply_keys = [&](f32x16 &x, int slot, int sub) {
+    // Operands: chunk 2 s + hh of key 32 sub + n32, chunk 4 sub + 2 u + hh of
+    // channel 32 j + n32.  The lane's part of the exchange and of the row is in
+    // the base; s, sub, u and j exchange further, by constants.
+    constexpr int KROW = D * 2, VROW = KT * 2;
+    const uint32_t at_k = 16 * key_chunk<D>(n32, hh), at_v = 16 * (2 * SLOT + value_chunk<D, KT>(n32, hh));
+    const uint8_t *const lds = reinterpret_cast<const uint8_t *>(s_kv);
+    const auto read_keys = [&](uint4 (&f)[S], int slot, int sub, int from, int to) SQ_INLINE {
+#pragma unroll
+        for (int s = from; s < to; ++s)
+            f[s] = *reinterpret_cast<const uint4 *>(lds + ((at_k ^ 32 * (s & 7)) + slot * (SLOT * 16)) +
+                                                    sub * 32 * KROW + (s & ~7) * 32);
+    };
+    const auto read_values = [&](uint4 (&f)[JT], int slot, int sub, int u) SQ_INLINE {
+#pragma unroll
+        for (int j = 0; j < JT; ++j) {
+            constexpr int kWays = D == 256 ? 8 : 16;
+            const int x = (4 * sub + 2 * u ^ value_exchange<D>(32 * j)) & (kWays - 1);
+            f[j] = *reinterpret_cast<const uint4 *>(lds + ((at_v ^ 16 * x) + slot * (SLOT * 16)) + j * 32 * VROW);
+        }
+    };
+    const auto multiply_keys = [&](f32x16 &x, const uint4 (&f)[S]) SQ_INLINE {
 #pragma unroll
         for (int i = 0; i < 16; ++i) x[i] = 0.0f;
 #pragma unroll
-        for (int s = 0; s < S; ++s)
-            x = mfma32<DT>(s_k[slot * SLOT + key_chunk<D>(32 * sub + n32, 2 * s + hh)], qf[s], x);
+        for (int s = 0; s < S; ++s) x = mfma32<DT>(f[s], qf[s], x);
     };
-    // The maximum that weights are taken against may trail the true one by 8
-    // (weights up to 256): rows are rescaled only where it is passed by more.
-    const auto take_maximum = [&](f32x16 &x, int t) {
+    const auto multiply_values = [&](const uint4 &w, const uint4 (&f)[JT]) SQ_INLINE {
+#pragma unroll
+        for (int j = 0; j < JT; ++j) o[j] = mfma32<DT>(f[j], w, o[j]);
+    };
+    const auto hide = [&](f32x16 &x, int t) SQ_INLINE {
         if (t < w_all_lo || t + 32 > w_all_hi) {
-            asm volatile("");
+            asm volatile("");  // (a branch, not selects)
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 const int key = t + (i & 3) + 8 * (i >> 2) + 4 * hh;
                 if (key < r_lo || key >= r_hi) x[i] = -INFINITY;
             }
         }
+    };
+    const auto largest = [&](const f32x16 &x) SQ_INLINE {
         float top = x[0];
 #pragma unroll
         for (int i = 1; i < 16; ++i) top = fmaxf(top, x[i]);
-        top *= c;
+        return top * c;
+    };
+    // The maximum that weights are taken against may trail the true one by 8
+    // (weights up to 256): rows are rescaled only where it is passed by more.
+    const auto rescale = [&](float top) SQ_INLINE {
         if (__any(top > m + 8.0f)) {
             const float mn = fmaxf(m, fmaxf(top, __shfl_xor(top, 32, 64)));
             const float f = __builtin_amdgcn_exp2f(m - mn);
@@ -255,7 +329,7 @@ __global__ __launch_bounds__(64 * NW, D < 256 ? 2 : 1) void kv_tile_kernel(const
             for (int j = 0; j < JT; ++j) o[j] *= f;
         }
     };
-    const auto form_weights = [&](f32x16 &x, Weights &w) {
+    const auto form_weights = [&](f32x16 &x, Weights &w) SQ_INLINE {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], c, -m));
@@ -266,15 +340,8 @@ __global__ __launch_bounds__(64 * NW, D < 256 ? 2 : 1) void kv_tile_kernel(const
             w.p[u] = make_uint4(pack16<DT>(x[8 * u], x[8 * u + 1]), pack16<DT>(x[8 * u + 2], x[8 * u + 3]),
                                 pack16<DT>(x[8 * u + 4], x[8 * u + 5]), pack16<DT>(x[8 * u + 6], x[8 * u + 7]));
     };
-    const auto multiply_values = [&](const Weights &w, int slot, int sub) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int j = 0; j < JT; ++j)
-                o[j] = mfma32<DT>(s_v[slot * SLOT + value_chunk<KT>(32 * j + n32, 4 * sub + 2 * u + hh)], w.p[u], o[j]);
-    };
     // (rare) The keys set apart, one at a time, for the rows that see them.
-    const auto add_apart = [&](const Weights &w, int t, uint32_t keys) {
+    const auto add_apart = [&](const Weights &w, int t, uint32_t keys) SQ_INLINE {
         for (; keys; keys &= keys - 1) {
             const int n = __builtin_ctz(keys), key = t + n;
             const int i = (n & 3) + 4 * (n >> 3), from = n32 + 32 * (n >> 2 & 1);
@@ -308,8 +375,8 @@ __global__ __launch_bounds__(64 * NW, D < 256 ? 2 : 1) void kv_tile_kernel(const
 
     if (tid < 2 * UNITS) s_apart[tid / UNITS][tid % UNITS] = 0;
     if (n_tiles > 0) {
-        page_k = page_of(tile_at(0) + sk);
-        page_v = page_of(tile_at(0) + 4 * sq4);
+        look_up_keys(0);
+        look_up_values(0);
         load_keys(0);
         load_values(0);
         __syncthreads();  // (s_apart)
@@ -320,32 +387,54 @@ __global__ __launch_bounds__(64 * NW, D < 256 ? 2 : 1) void kv_tile_kernel(const
         __syncthreads();
         f32x16 x[2];
         Weights w;
-        multiply_keys(x[0], 0, 0);
-        take_maximum(x[0], tile_at(0));
+        uint4 kf[S], vf[2][JT];
+        read_keys(kf, 0, 0, 0, S);
+        multiply_keys(x[0], kf);
+        read_keys(kf, 0, 1, 0, S / 2);
+        hide(x[0], tile_at(0));
+        rescale(largest(x[0]));
         for (int i = 0; i < n_tiles; ++i) {
             const int t = tile_at(i), slot = i & 1;
-#pragma unroll
-            for (int u = 0; u < UNITS; ++u) {
-                // unit u is weighted, the next one scored
-                const bool last = u == UNITS - 1;
-                multiply_keys(x[~u & 1], last ? slot ^ 1 : slot, last ? 0 : u + 1);
+            // Unit u of the tile is weighted, the next one (whose keys' operands
+            // are read) scored, and the operands of the one after it read.
+            const auto unit = [&](auto number) SQ_INLINE {
+                constexpr int u = decltype(number)::value;
+                constexpr bool last = u == UNITS - 1;
+                read_keys(kf, last ? slot ^ 1 : slot, (u + 1) % UNITS, S / 2, S);
+                read_values(vf[0], slot, u, 0);
+                __builtin_amdgcn_sched_barrier(0);
+                multiply_keys(x[~u & 1], kf);
                 form_weights(x[u & 1], w);
-                multiply_values(w, slot, u);
-                if (u == 0) {
+                mfma_with<S, 56 / S>();
+                __builtin_amdgcn_sched_barrier(0);
+                hide(x[~u & 1], last ? tile_at(i + 1) : t + 32 * (u + 1));
+                read_values(vf[1], slot, u, 1);
+                multiply_values(w.p[0], vf[0]);
+                if constexpr (u == 0) {
                     stage_keys(slot ^ 1);
                     load_keys(i + 2);
                     if (tid < UNITS) s_apart[slot ^ 1][tid] = 0;
                 }
-                if (last) {
+                if constexpr (u == (UNITS == 4 ? 2 : 1)) {
                     stage_values(i + 1, slot ^ 1);
                     load_values(i + 2);
                 }
+                // The first barrier stands between the staging of the next keys
+                // and their reading, the second the values'; either also between
+                // the last reads of a slot and its staging.
+                if constexpr (u == 0 || u == (UNITS == 4 ? 2 : 1)) lds_barrier();
+                read_keys(kf, u + 2 < UNITS ? slot : slot ^ 1, (u + 2) % UNITS, 0, S / 2);
                 const uint32_t apart = __builtin_amdgcn_readfirstlane(s_apart[slot][u]);
+                multiply_values(w.p[1], vf[1]);
+                const float top = largest(x[~u & 1]);
                 if (apart) add_apart(w, t + 32 * u, apart);
-                take_maximum(x[~u & 1], last ? tile_at(i + 1) : t + 32 * (u + 1));
-                // the next tile's keys are read from the last unit on, its values
-                // from the first of the next
-                if (u >= UNITS - 2) __syncthreads();
+                rescale(top);
+            };
+            unit(std::integral_constant<int, 0>{});
+            unit(std::integral_constant<int, 1>{});
+            if constexpr (UNITS == 4) {
+                unit(std::integral_constant<int, 2>{});
+                unit(std::integral_constant<int, 3>{});
             }
         }
     }
