@@ -58,8 +58,8 @@ class _KvCache(ctypes.Structure):
                 ("page", _I64), ("dim", _I64), ("fmt", _I)]
 
 
-_STRIDES = _I64 * 2
-_CACHE_P, _STRIDE_P = ctypes.POINTER(_KvCache), ctypes.POINTER(_I64)
+_CACHE_P = ctypes.POINTER(_KvCache)
+_Strides2, _Strides6 = _I64 * 2, _I64 * 6
 
 SIGNATURES = {
     "sq_status_str": (ctypes.c_char_p, [_I]),
@@ -90,10 +90,10 @@ SIGNATURES = {
     "sq_dequantize_mx": (_I, [_P, _P, _I, _I64, _I64, _P, _I, _P]),
     "sq_gemm_mxfp4": (_I, [_P, _P, _I, _P, _P, _I64, _I64, _I64, _P, _I, _P]),
     # the microscaled cache (include/sq_kv.h)
-    "sq_rope_quantize_kv_mx": (_I, [_P, _STRIDE_P, _P, _STRIDE_P, _P, _STRIDE_P, _I, _I64, _I64, _P,
+    "sq_rope_quantize_kv_mx": (_I, [_P, _P, _P, _P, _P, _P, _I, _I64, _I64, _P,
                                     _P, _I64, ctypes.c_double, _I, _P, _P, _P, _CACHE_P, _P, _P]),
     "sq_dequantize_kv_mx": (_I, [_CACHE_P, _P, _I64, _I64, _P, _I64, _P, _P, _I, _P]),
-    "sq_attention_kv_mx": (_I, [_P, _STRIDE_P, _I, _I64, _I64, _CACHE_P, _P, _I64, _I64, _P, _P, _I64,
+    "sq_attention_kv_mx": (_I, [_P, _P, _I, _I64, _I64, _CACHE_P, _P, _I64, _I64, _P, _P, _I64,
                                 _F, _I, _I64, _P, _P, ctypes.c_size_t, _P]),
     "sq_attention_kv_mx_workspace": (ctypes.c_size_t, [_I64, _I64, _CACHE_P, _I64, _I64, _I64]),
     # coverage entry point (include/sq_mx_test.h): the pipelined product's block shape forced
@@ -137,15 +137,18 @@ def lib():
 
 _torch_mod = None
 _raw_stream = None  # torch's current-stream handle by device, where it has one
+_current_gpu = None  # the current device's number
 _dt_codes = {}
 
 
 def _torch():
-    global _torch_mod, _raw_stream
+    global _torch_mod, _raw_stream, _current_gpu
     if _torch_mod is None:
         import torch
 
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        # (torch.cuda.current_device asks this, 0.4 us later)
+        _current_gpu = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
         _dt_codes.update({torch.float32: SQ_F32, torch.float16: SQ_F16, torch.bfloat16: SQ_BF16})
         _torch_mod = torch
     return _torch_mod
@@ -511,7 +514,7 @@ def _mx_call(name, tensors, args, stream, *last):
             raise ValueError(f"operands on {tensors[0].device} and {t.device}")
     if stream is not None and stream.device.index != dev:
         raise ValueError(f"operands on {tensors[0].device}, stream on {stream.device}")
-    if _torch_mod.cuda.current_device() == dev:
+    if _current_gpu() == dev:
         if stream is None and _raw_stream is not None:
             status = fn(*args, _raw_stream(dev), *last)
         else:
@@ -736,37 +739,43 @@ def _kv_cache(cache, fmt):
     """The C form of a cache (kq, ks, vq, vs)."""
     u8 = _torch().uint8
     kq, ks, vq, vs = cache
-    for t, name in ((kq, "cached keys"), (ks, "the keys' scales"), (vq, "cached values"),
-                    (vs, "the values' scales")):
-        _mx_check(t, name, (u8,), 4)
     shape, blocks = kq.shape, ks.shape
-    dim = blocks[3] * 32
-    if (vq.shape != shape or vs.shape != blocks or shape[:3] != blocks[:3]
-            or shape[3] != _mx_codes(fmt, dim)):
+    if not (len(shape) == 4 == len(blocks) and vq.shape == shape and vs.shape == blocks
+            and shape[:3] == blocks[:3] and shape[3] == _mx_codes(fmt, blocks[3] * 32)
+            and kq.dtype == u8 == ks.dtype and vq.dtype == u8 == vs.dtype
+            and kq.is_contiguous() and ks.is_contiguous() and vq.is_contiguous()
+            and vs.is_contiguous() and kq.is_cuda):
+        for t, name in ((kq, "cached keys"), (ks, "the keys' scales"), (vq, "cached values"),
+                        (vs, "the values' scales")):
+            _check(t, name, (u8,), 4)
         raise ValueError(f"cache of codes {tuple(shape)}, {tuple(vq.shape)} and scales "
                          f"{tuple(blocks)}, {tuple(vs.shape)}: they disagree")
-    return _KvCache(kq.data_ptr(), ks.data_ptr(), vq.data_ptr(), vs.data_ptr(), shape[0], shape[1],
-                    shape[2], dim, fmt)
+    pages, heads, page, n = blocks
+    return _KvCache(kq.data_ptr(), ks.data_ptr(), vq.data_ptr(), vs.data_ptr(), pages, heads, page,
+                    n * 32, fmt)
 
 
 def _kv_rows(x, name, dim, dtypes):
-    """(pointer, strides) of rows [T, heads, dim], each dense."""
-    if not (x.is_cuda and x.dtype in dtypes and x.dim() == 3 and x.stride(2) == 1):
+    """The token's and the head's stride of rows [T, heads, dim], each dense."""
+    if not (x.dtype in dtypes and x.dim() == 3 and x.is_cuda):
         if not x.is_cuda:
             raise ValueError(f"{name} must be a GPU tensor")
         if x.dtype not in dtypes:
             raise ValueError(f"{name}: dtype {x.dtype} not in {tuple(dtypes)}")
-        raise ValueError(f"{name} must be [tokens, heads, {dim}] with dense rows")
+        raise ValueError(f"{name} must be [tokens, heads, {dim}]")
+    token, head, one = x.stride()
     if x.shape[2] != dim:
         raise ValueError(f"{name} has rows of {x.shape[2]} channels, the cache of {dim}")
-    return x.data_ptr(), _STRIDES(x.stride(0), x.stride(1))
+    if one != 1:
+        raise ValueError(f"{name} must have dense rows")
+    return token, head
 
 
 def _kv_ints(t, name, dtype, shape):
     """The pointer of an integer tensor of this shape, or None."""
     if t is None:
         return None
-    if not (t.is_cuda and t.dtype == dtype and t.is_contiguous() and t.shape == shape):
+    if not (t.dtype == dtype and t.shape == shape and t.is_contiguous() and t.is_cuda):
         _check(t, name, (dtype,), len(shape))
         raise ValueError(f"{name} {tuple(t.shape)} is not {tuple(shape)}")
     return t.data_ptr()
@@ -776,7 +785,7 @@ def _kv_mul(t, name, heads, dim):
     """The pointer of fp32 multipliers [heads, dim] (or as one vector), or None."""
     if t is None:
         return None
-    if not (t.is_cuda and t.dtype == _torch_mod.float32 and t.is_contiguous()):
+    if not (t.dtype == _torch_mod.float32 and t.is_contiguous() and t.is_cuda):
         _check(t, name, (_torch_mod.float32,))
     if t.shape != (heads, dim) and t.shape != (heads * dim,):
         raise ValueError(f"{name} {tuple(t.shape)} is not {(heads, dim)}")
@@ -786,8 +795,10 @@ def _kv_mul(t, name, heads, dim):
 def _kv_result(out, name, shape, dtype, device, stream):
     """A dense output [tokens, heads, dim]: `out`, checked, or a new one."""
     if out is None:
-        rows, heads, dim = shape
-        return _mx_empty(rows, heads * dim, dtype, device, stream).view(shape)
+        if stream is not None:  # (of that stream's memory: _mx_empty)
+            with _torch_mod.cuda.stream(stream):
+                return _kv_result(None, name, shape, dtype, device, None)
+        return _torch_mod.empty_strided(shape, (shape[1] * shape[2], shape[2], 1), dtype=dtype, device=device)
     if not (out.is_cuda and out.dtype == dtype and out.is_contiguous() and out.shape == shape):
         _check(out, name, (dtype,), 3)
         raise ValueError(f"{name} {tuple(out.shape)} is not {tuple(shape)}")
@@ -806,8 +817,8 @@ def rope_quantize_kv_mx(q, k, v, slots, cache, fmt=SQ_MX_E2M1, positions=None, i
     c = _kv_cache(cache, fmt)
     heads, dim = c.heads, c.dim
     dt = k.dtype
-    kp, k_stride = _kv_rows(k, "k", dim, _dt_codes)
-    vp, v_stride = _kv_rows(v, "v", dim, (dt,))
+    k_token, k_head = _kv_rows(k, "k", dim, _dt_codes)
+    v_token, v_head = _kv_rows(v, "v", dim, (dt,))
     T = k.shape[0]
     if k.shape[1] != heads or v.shape != k.shape:
         raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)} do not fit a cache of {heads} heads")
@@ -824,20 +835,24 @@ def rope_quantize_kv_mx(q, k, v, slots, cache, fmt=SQ_MX_E2M1, positions=None, i
         rotary, fp = 2 * inv_freq.shape[0], inv_freq.data_ptr()
         if rotary > dim or rotary % 16:
             raise ValueError(f"{rotary} rotated channels: a multiple of 16 up to {dim} is needed")
-    qp, q_stride, q_heads, y = None, None, 0, None
+    qp, yp, q_heads, y, q_token, q_head = None, None, 0, None, 0, 0
     if q is not None:
-        qp, q_stride = _kv_rows(q, "q", dim, (dt,))
-        q_heads = q.shape[1]
-        if q.shape[0] != T:
-            raise ValueError(f"q has {q.shape[0]} tokens, k {T}")
+        q_token, q_head = _kv_rows(q, "q", dim, (dt,))
+        q_tokens, q_heads, _ = q.shape
+        if q_tokens != T:
+            raise ValueError(f"q has {q_tokens} tokens, k {T}")
+        qp = q.data_ptr()
         y = _kv_result(out, "out", (T, q_heads, dim), dt, q.device, stream)
+        yp = y.data_ptr()
     elif q_mul is not None or out is not None:
         raise ValueError("q_mul and out need q")
     qm, km = _kv_mul(q_mul, "q_mul", q_heads, dim), _kv_mul(k_mul, "k_mul", heads, dim)
+    strides = _Strides6(q_token, q_head, k_token, k_head, v_token, v_head)
+    at = ctypes.addressof(strides)
     _mx_call("sq_rope_quantize_kv_mx",
-             (k, v, q, slots, positions if rotary else None, inv_freq, q_mul, k_mul, y) + tuple(cache),
-             (qp, q_stride, kp, k_stride, vp, v_stride, _dt_codes[dt], T, q_heads, pp, fp, rotary,
-              amplitude, layout, qm, km, sp, c, _ptr(y)), stream)
+             (k, v, q, slots, positions if rotary else None, inv_freq, q_mul, k_mul, y, *cache),
+             (qp, at, k.data_ptr(), at + 16, v.data_ptr(), at + 32, _dt_codes[dt], T, q_heads, pp, fp,
+              rotary, amplitude, layout, qm, km, sp, c, yp), stream)
     return y
 
 
@@ -865,7 +880,7 @@ def dequantize_kv_mx(cache, table, cu, total, fmt=SQ_MX_E2M1, out_dtype=None, ou
             raise ValueError(f"out: dtype {dtype} not in {tuple(_dt_codes)}")
     k = _kv_result(None if out is None else out[0], "out", shape, dtype, table.device, stream)
     v = _kv_result(None if out is None else out[1], "out", shape, dtype, table.device, stream)
-    _mx_call("sq_dequantize_kv_mx", (table, cu, k, v) + tuple(cache),
+    _mx_call("sq_dequantize_kv_mx", (table, cu, k, v, *cache),
              (c, table.data_ptr(), B, width, cp, shape[0], k.data_ptr(), v.data_ptr(),
               _dt_codes[dtype]), stream)
     return k, v
@@ -889,8 +904,8 @@ def attention_kv_mx(q, cache, table, seq_lens, cu_q=None, fmt=SQ_MX_E2M1, max_q=
     c = _kv_cache(cache, fmt)
     dim = c.dim
     torch = _torch_mod
-    qp, q_stride = _kv_rows(q, "q", dim, (torch.float16, torch.bfloat16))
-    T, q_heads = q.shape[0], q.shape[1]
+    strides = _Strides2(*_kv_rows(q, "q", dim, (torch.float16, torch.bfloat16)))
+    T, q_heads, _ = q.shape
     if q_heads == 0 or q_heads % c.heads:
         raise ValueError(f"{q_heads} query heads do not share {c.heads} key heads evenly")
     i32 = torch.int32
@@ -917,8 +932,8 @@ def attention_kv_mx(q, cache, table, seq_lens, cu_q=None, fmt=SQ_MX_E2M1, max_q=
         workspace = _mx_empty(1, need, torch.uint8, q.device, stream)
     else:
         _check(workspace, "workspace", (torch.uint8,))
-    _mx_call("sq_attention_kv_mx", (q, table, seq_lens, cu_q, y, workspace) + tuple(cache),
-             (qp, q_stride, _dt_codes[q.dtype], T, q_heads, c, table.data_ptr(), B, width, lp, cp,
-              max_q, scale, 1 if causal else 0, window, y.data_ptr(), workspace.data_ptr(),
-              workspace.numel(), ), stream)
+    _mx_call("sq_attention_kv_mx", (q, table, seq_lens, cu_q, y, workspace, *cache),
+             (q.data_ptr(), ctypes.addressof(strides), _dt_codes[q.dtype], T, q_heads, c,
+              table.data_ptr(), B, width, lp, cp, max_q, scale, 1 if causal else 0, window,
+              y.data_ptr(), workspace.data_ptr(), workspace.numel()), stream)
     return y
