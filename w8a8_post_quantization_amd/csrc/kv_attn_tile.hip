@@ -32,12 +32,13 @@ template <int D>
 __device__ __forceinline__ int key_chunk(int key, int ch) {
     return key * (D / 8) + (ch ^ (D == 64 ? key >> 1 & 7 : key & 15));
 }
-template <int D>
+template <int D, int KT>
 __device__ __forceinline__ int value_exchange(int d) {
-    return D == 64 ? (d ^ d >> 2) & 15 : D == 128 ? (d ^ d >> 3) & 15 : (d >> 1 ^ d >> 4) & 7;
+    constexpr int kPart = D == 64 ? 2 : D == 128 ? 3 : 4;  // log2(D / 16)
+    return KT == 128 ? (d ^ d >> kPart) & 15 : (d >> 1 ^ d >> kPart) & 7;
 }
 template <int D, int KT>
-__device__ __forceinline__ int value_chunk(int d, int ch) { return d * (KT / 8) + (ch ^ value_exchange<D>(d)); }
+__device__ __forceinline__ int value_chunk(int d, int ch) { return d * (KT / 8) + (ch ^ value_exchange<D, KT>(d)); }
 
 // The order of what follows the last scheduling barrier: a matrix instruction,
 // N vector instructions, R times.
@@ -54,7 +55,7 @@ template <int D, int FMT, int DT, int NW>
 __global__ __launch_bounds__(64 * NW, D < 256 ? 2 : 1) void kv_tile_kernel(const KvAttention a, int rows_min, int splits,
                                                          float *parts, const int32_t *__restrict__ tables) {
     constexpr int NB = D / 32, S = D / 16, JT = D / 32, R = 32 * NW;
-    constexpr int KT = D < 256 ? 128 : 64, UNITS = KT / 32, NT = 64 * NW;  // keys, units of a tile; threads
+    constexpr int KT = D < 256 && NW == 8 ? 128 : 64, UNITS = KT / 32, NT = 64 * NW;  // keys, units of a tile; threads
     constexpr int PASS = 4 * KT / NT;  // times that a thread stages
     constexpr int RB = FMT == E2M1 ? D / 2 : D;
     // As a thread stages a tile: of one key a quarter of the channels, and of
@@ -65,7 +66,7 @@ __global__ __launch_bounds__(64 * NW, D < 256 ? 2 : 1) void kv_tile_kernel(const
     constexpr int SLOT = KT * D / 8;  // chunks of 16 bytes
     __shared__ __attribute__((aligned(1024))) uint4 s_kv[4 * SLOT];
     uint4 *const s_k = s_kv, *const s_v = s_kv + 2 * SLOT;
-    __shared__ int s_pre[NT + 1], s_at[2];
+    __shared__ int s_pre[NT + 1], s_wave[NW], s_at[2];
     __shared__ uint32_t s_apart[2][UNITS];
 
     const int tid = threadIdx.x, lane = tid & 63;
@@ -84,15 +85,17 @@ __global__ __launch_bounds__(64 * NW, D < 256 ? 2 : 1) void kv_tile_kernel(const
     {
         int sum = 0;
         for (int i = 0; i < per_thread && b_first + i < a.B; ++i) sum += tiles_of(kv_seq(a, b_first + i));
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) {
+            const int v = __shfl_up(sum, off, 64);
+            if (lane >= off) sum += v;
+        }
+        if (lane == 63) s_wave[wave] = sum;
+        __syncthreads();
+        for (int w = 0; w < wave; ++w) sum += s_wave[w];
         s_pre[tid + 1] = sum;
         if (tid == 0) s_pre[0] = 0;
         __syncthreads();
-        for (int off = 1; off < NT; off <<= 1) {
-            const int v = tid >= off ? s_pre[tid + 1 - off] : 0;
-            __syncthreads();
-            s_pre[tid + 1] += v;
-            __syncthreads();
-        }
     }
     const int want = s_pre[NT] - 1 - (int)(blockIdx.x / heads);
     if (want < 0) return;
@@ -270,7 +273,7 @@ __global__ __launch_bounds__(64 * NW, D < 256 ? 2 : 1) void kv_tile_kernel(const
     };
 
     // Scores of 32 keys, their largest, the weights, the weighted values.
-    struct Weights { uint4 p[2]; };
+    struct Weights { u4v p[2]; };
     // Operands: chunk 2 s + hh of key 32 sub + n32, chunk 4 sub + 2 u + hh of
     // channel 32 j + n32.  The lane's part of the exchange and of the row is in
     // the base; s, sub, u and j exchange further, by constants.
@@ -286,8 +289,7 @@ __global__ __launch_bounds__(64 * NW, D < 256 ? 2 : 1) void kv_tile_kernel(const
     const auto read_values = [&](uint4 (&f)[JT], int slot, int sub, int u) SQ_INLINE {
 #pragma unroll
         for (int j = 0; j < JT; ++j) {
-            constexpr int kWays = D == 256 ? 8 : 16;
-            const int x = (4 * sub + 2 * u ^ value_exchange<D>(32 * j)) & (kWays - 1);
+            const int x = (4 * sub + 2 * u ^ value_exchange<D, KT>(32 * j)) & (KT / 8 - 1);
             f[j] = *reinterpret_cast<const uint4 *>(lds + ((at_v ^ 16 * x) + slot * (SLOT * 16)) + j * 32 * VROW);
         }
     };
@@ -297,9 +299,9 @@ __global__ __launch_bounds__(64 * NW, D < 256 ? 2 : 1) void kv_tile_kernel(const
 #pragma unroll
         for (int s = 0; s < S; ++s) x = mfma32<DT>(f[s], qf[s], x);
     };
-    const auto multiply_values = [&](const uint4 &w, const uint4 (&f)[JT]) SQ_INLINE {
+    const auto multiply_values = [&](const u4v &w, const uint4 (&f)[JT]) SQ_INLINE {
 #pragma unroll
-        for (int j = 0; j < JT; ++j) o[j] = mfma32<DT>(f[j], w, o[j]);
+        for (int j = 0; j < JT; ++j) o[j] = mfma32<DT>(f[j], make_uint4(w.x, w.y, w.z, w.w), o[j]);
     };
     const auto hide = [&](f32x16 &x, int t) SQ_INLINE {
         if (t < w_all_lo || t + 32 > w_all_hi) {
@@ -337,8 +339,8 @@ __global__ __launch_bounds__(64 * NW, D < 256 ? 2 : 1) void kv_tile_kernel(const
         }
 #pragma unroll
         for (int u = 0; u < 2; ++u)
-            w.p[u] = make_uint4(pack16<DT>(x[8 * u], x[8 * u + 1]), pack16<DT>(x[8 * u + 2], x[8 * u + 3]),
-                                pack16<DT>(x[8 * u + 4], x[8 * u + 5]), pack16<DT>(x[8 * u + 6], x[8 * u + 7]));
+            w.p[u] = u4v{pack16<DT>(x[8 * u], x[8 * u + 1]), pack16<DT>(x[8 * u + 2], x[8 * u + 3]),
+                         pack16<DT>(x[8 * u + 4], x[8 * u + 5]), pack16<DT>(x[8 * u + 6], x[8 * u + 7])};
     };
     // (rare) The keys set apart, one at a time, for the rows that see them.
     const auto add_apart = [&](const Weights &w, int t, uint32_t keys) SQ_INLINE {
@@ -393,6 +395,7 @@ __global__ __launch_bounds__(64 * NW, D < 256 ? 2 : 1) void kv_tile_kernel(const
         read_keys(kf, 0, 1, 0, S / 2);
         hide(x[0], tile_at(0));
         rescale(largest(x[0]));
+        wait_vmcnt<0>();  // (else the queries' loads count as pending in the loop)
         for (int i = 0; i < n_tiles; ++i) {
             const int t = tile_at(i), slot = i & 1;
             // Unit u of the tile is weighted, the next one (whose keys' operands
@@ -405,6 +408,8 @@ __global__ __launch_bounds__(64 * NW, D < 256 ? 2 : 1) void kv_tile_kernel(const
                 __builtin_amdgcn_sched_barrier(0);
                 multiply_keys(x[~u & 1], kf);
                 form_weights(x[u & 1], w);
+                // (kept here: the compiler would move the weights behind the branches)
+                asm volatile("" : "+v"(w.p[0]), "+v"(w.p[1]), "+v"(l));
                 mfma_with<S, 56 / S>();
                 __builtin_amdgcn_sched_barrier(0);
                 hide(x[~u & 1], last ? tile_at(i + 1) : t + 32 * (u + 1));
@@ -427,7 +432,12 @@ __global__ __launch_bounds__(64 * NW, D < 256 ? 2 : 1) void kv_tile_kernel(const
                 const uint32_t apart = __builtin_amdgcn_readfirstlane(s_apart[slot][u]);
                 multiply_values(w.p[1], vf[1]);
                 const float top = largest(x[~u & 1]);
-                if (apart) add_apart(w, t + 32 * u, apart);
+                if (apart) {
+                    add_apart(w, t + 32 * u, apart);
+                    // (loads of it that are left unused would be waited for below,
+                    // whether it ran or not)
+                    wait_vmcnt<0>();
+                }
                 rescale(top);
             };
             unit(std::integral_constant<int, 0>{});
