@@ -582,10 +582,13 @@ static Plan plan_attention(int64_t T, int q_heads, int heads, int dim, int fmt, 
         p.bytes = kMaxBlocks * sizeof(Part) + (size_t)p.blocks * 2 * 16 * p.nt * (dim + 2) * sizeof(float);
     }
     if (most > 32) {
-        p.waves = dim == 256 || most <= 128 ? 4 : 8;
+        p.waves = dim != 128 || most <= 128 ? 4 : 8;
+        // Blocks that the GPU holds at once (kv_attn_tile.hip: registers allow two
+        // waves a SIMD, three of 64 channels, one of 256).  Where there are less
+        // than half of them, the keys of each tile are split over blocks.
+        const int64_t slots = kCus * (dim == 64 ? 3 : dim == 128 && p.waves == 4 ? 2 : 1);
         const int64_t tiles = (T * group + 32 * p.waves - 1) / (32 * p.waves) * heads;
-        // few tiles: the keys of each are split over blocks
-        int64_t splits = tiles >= 256 ? 1 : 512 / tiles;
+        int64_t splits = slots / tiles;
         if (splits > (keys + 511) / 512) splits = (keys + 511) / 512;
         p.splits = (int)(splits > 16 ? 16 : splits < 1 ? 1 : splits);
         p.tile_parts = (p.bytes + 255) & ~(size_t)255;

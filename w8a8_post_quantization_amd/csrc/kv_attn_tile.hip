@@ -52,11 +52,11 @@ __device__ __forceinline__ void mfma_with() {
 }
 
 template <int D, int FMT, int DT, int NW>
-__global__ __launch_bounds__(64 * NW, D < 256 ? 2 : 1) void kv_tile_kernel(const KvAttention a, int rows_min, int splits,
+__global__ __launch_bounds__(64 * NW, D == 64 ? 3 : D == 128 ? 2 : 1) void kv_tile_kernel(const KvAttention a, int rows_min, int splits,
                                                          float *parts, const int32_t *__restrict__ tables) {
     constexpr int NB = D / 32, S = D / 16, JT = D / 32, R = 32 * NW;
     constexpr int KT = D < 256 && NW == 8 ? 128 : 64, UNITS = KT / 32, NT = 64 * NW;  // keys, units of a tile; threads
-    constexpr int PASS = 4 * KT / NT;  // times that a thread stages
+    static_assert(4 * KT == NT, "a tile is staged by all threads once");
     constexpr int RB = FMT == E2M1 ? D / 2 : D;
     // As a thread stages a tile: of one key a quarter of the channels, and of
     // four successive keys a sixteenth of the values' channels.
@@ -65,7 +65,6 @@ __global__ __launch_bounds__(64 * NW, D < 256 ? 2 : 1) void kv_tile_kernel(const
     constexpr int VN = RB / 16, VC = D / 16;
     constexpr int SLOT = KT * D / 8;  // chunks of 16 bytes
     __shared__ __attribute__((aligned(1024))) uint4 s_kv[4 * SLOT];
-    uint4 *const s_k = s_kv, *const s_v = s_kv + 2 * SLOT;
     __shared__ int s_pre[NT + 1], s_wave[NW], s_at[2];
     __shared__ uint32_t s_apart[2][UNITS];
 
@@ -97,7 +96,9 @@ __global__ __launch_bounds__(64 * NW, D < 256 ? 2 : 1) void kv_tile_kernel(const
         if (tid == 0) s_pre[0] = 0;
         __syncthreads();
     }
-    const int want = s_pre[NT] - 1 - (int)(blockIdx.x / heads);
+    // (blocks of no tile are the last: among others they would upset the
+    // distribution over the CUs, 150 us for 86 with every third block empty)
+    const int want = s_pre[NT] - 1 - (int)(blockIdx.x / (heads * splits));
     if (want < 0) return;
     if (s_pre[tid] <= want && want < s_pre[tid + 1]) {
         int before = s_pre[tid], b = b_first;
@@ -113,7 +114,7 @@ __global__ __launch_bounds__(64 * NW, D < 256 ? 2 : 1) void kv_tile_kernel(const
     __syncthreads();
     const int b = __builtin_amdgcn_readfirstlane(s_at[0]);
     const int tile = __builtin_amdgcn_readfirstlane(s_at[1]);
-    const int h = blockIdx.x % heads, split = blockIdx.y;
+    const int h = blockIdx.x % heads, split = blockIdx.x / heads % splits;
     const KvSeq seq = kv_seq(a, b);
     const int rows = seq.nq * group;  // (T * q_heads < 2^31)
 
@@ -171,14 +172,13 @@ __global__ __launch_bounds__(64 * NW, D < 256 ? 2 : 1) void kv_tile_kernel(const
     const int g_last = (t_hi - 1) >> 4;
 
     // Loads of a tile into registers; tiles past the last are the last again.
-    // (pass p of a thread: key sk + p NT / 4, keys 4 (sq4 + p NT / 16) ..)
     const int sk = tid >> 2, sc = tid & 3, sq4 = tid >> 4, sn = tid & 15;
-    Words<KN> rk[PASS];
-    uint32_t rks[PASS][KS];
-    Words<VN> rv[PASS][4];
-    uint32_t rvs[PASS][4];
-    uint32_t nan_k[PASS], nan_v[PASS];  // 255 where the page is not in the cache
-    int page_k[PASS], page_v[PASS];     // of the next tile to load
+    Words<KN> rk;
+    uint32_t rks[KS];
+    Words<VN> rv[4];
+    uint32_t rvs[4];
+    uint32_t nan_k, nan_v;  // 255 where the page is not in the cache
+    int page_k, page_v;     // of the next tile to load
     const auto tile_at = [&](int i) SQ_INLINE { return t_base + (k0 + (i < n_tiles ? i : n_tiles - 1)) * KT; };
     const auto group_of = [&](int key) SQ_INLINE { return key >> 4 < g_last ? key >> 4 : g_last; };
     const auto page_of = [&](int key) SQ_INLINE { return table[group_of(key) >> (plog - 4)]; };
@@ -187,87 +187,80 @@ __global__ __launch_bounds__(64 * NW, D < 256 ? 2 : 1) void kv_tile_kernel(const
         nan = held ? 0u : 255u;
         return kv_row(a.cache, held ? page : 0, h, ((group_of(key) & ((1 << (plog - 4)) - 1)) << 4) + (key & 15));
     };
-    const auto look_up_keys = [&](int i) SQ_INLINE {
-#pragma unroll
-        for (int p = 0; p < PASS; ++p) page_k[p] = page_of(tile_at(i) + sk + p * (NT / 4));
-    };
-    const auto look_up_values = [&](int i) SQ_INLINE {
-#pragma unroll
-        for (int p = 0; p < PASS; ++p) page_v[p] = page_of(tile_at(i) + 4 * (sq4 + p * (NT / 16)));
-    };
     const auto load_keys = [&](int i) SQ_INLINE {
+        const int64_t at = row_of(tile_at(i) + sk, page_k, nan_k);
+        rk = load_codes<KN>(a.cache.kq + at * RB + sc * KN);
 #pragma unroll
-        for (int p = 0; p < PASS; ++p) {
-            const int64_t at = row_of(tile_at(i) + sk + p * (NT / 4), page_k[p], nan_k[p]);
-            rk[p] = load_codes<KN>(a.cache.kq + at * RB + sc * KN);
-#pragma unroll
-            for (int z = 0; z < KS; ++z) rks[p][z] = a.cache.ks[at * NB + sc * KC / 32 + z];
-        }
-        look_up_keys(i + 1);
+        for (int z = 0; z < KS; ++z) rks[z] = a.cache.ks[at * NB + sc * KC / 32 + z];
+        page_k = page_of(tile_at(i + 1) + sk);
     };
     const auto load_values = [&](int i) SQ_INLINE {
+        const int64_t at = row_of(tile_at(i) + 4 * sq4, page_v, nan_v);
 #pragma unroll
-        for (int p = 0; p < PASS; ++p) {
-            const int64_t at = row_of(tile_at(i) + 4 * (sq4 + p * (NT / 16)), page_v[p], nan_v[p]);
-#pragma unroll
-            for (int z = 0; z < 4; ++z) {
-                rv[p][z] = load_codes<VN>(a.cache.vq + (at + z) * RB + sn * VN);
-                rvs[p][z] = a.cache.vs[(at + z) * NB + sn * VC / 32];
-            }
+        for (int z = 0; z < 4; ++z) {
+            rv[z] = load_codes<VN>(a.cache.vq + (at + z) * RB + sn * VN);
+            rvs[z] = a.cache.vs[(at + z) * NB + sn * VC / 32];
         }
-        look_up_values(i + 1);
+        page_v = page_of(tile_at(i + 1) + 4 * sq4);
     };
+    // In LDS a lane's place is kept as one base, and its other places formed
+    // from it as they are needed (exchanged by constants, at constant distances):
+    // the compiler is kept from holding them all.
+    constexpr int KROW = D * 2, VROW = KT * 2, SLOTB = SLOT * 16;
+    uint8_t *const lds = reinterpret_cast<uint8_t *>(s_kv);
+    const auto place_of = [&](uint32_t base, int slot) SQ_INLINE {
+        base += slot * SLOTB;
+        asm("" : "+v"(base));
+        return base;
+    };
+    const uint32_t to_k = 16 * key_chunk<D>(sk, sc * (KC / 8));
+    const uint32_t to_v = 2 * SLOTB + 16 * value_chunk<D, KT>(sn * VC, (sq4 >> 2) * 2 + (sq4 & 1)) + 8 * ((sq4 & 3) >> 1);
     const auto stage_keys = [&](int slot) SQ_INLINE {
+        const uint32_t to = place_of(to_k, slot);
 #pragma unroll
-        for (int p = 0; p < PASS; ++p)
-#pragma unroll
-            for (int z = 0; z < KC / 8; ++z) {
-                const float s = e8m0(rks[p][KC < 32 ? 0 : z / 4] | nan_k[p]);
-                s_k[slot * SLOT + key_chunk<D>(sk + p * (NT / 4), sc * (KC / 8) + z)] =
-                    codes8_to_16<FMT, DT>(&rk[p].w[z * (FMT == E2M1 ? 1 : 2)], s);
-            }
+        for (int z = 0; z < KC / 8; ++z) {
+            const float s = e8m0(rks[KC < 32 ? 0 : z / 4] | nan_k);
+            *reinterpret_cast<uint4 *>(lds + (to ^ 16 * z)) = codes8_to_16<FMT, DT>(&rk.w[z * (FMT == E2M1 ? 1 : 2)], s);
+        }
     };
     const auto stage_values = [&](int i, int slot) SQ_INLINE {
         const int t = tile_at(i);
 #pragma unroll
-        for (int p = 0; p < PASS; ++p) {
-            const int quad = sq4 + p * (NT / 16);
+        for (int z = 0; z < 4; ++z) rvs[z] |= nan_v;
+        if (t < t_all_lo || t + KT > t_all_hi) {
+            asm volatile("");  // (a branch, not selects)
+            // Keys that no row of the block sees (behind the last, before the
+            // window) are taken as 0: what their place holds may be anything.
+            // Where an infinity or NaN may be, it is set apart: a weight of 0
+            // does not keep it from a row that must not see it.
 #pragma unroll
-            for (int z = 0; z < 4; ++z) rvs[p][z] |= nan_v[p];
-            if (t < t_all_lo || t + KT > t_all_hi) {
-                asm volatile("");  // (a branch, not selects)
-                // Keys that no row of the block sees (behind the last, before the
-                // window) are taken as 0: what their place holds may be anything.
-                // Where an infinity or NaN may be, it is set apart: a weight of 0
-                // does not keep it from a row that must not see it.
-#pragma unroll
-                for (int z = 0; z < 4; ++z) {
-                    const int key = 4 * quad + z;
-                    const bool none = t + key < t_lo || t + key >= t_hi;
-                    const bool alone = !none && may_be_nonfinite<FMT, DT>(rv[p][z], rvs[p][z]);
-                    if (alone) atomicOr(&s_apart[slot][key >> 5], 1u << (key & 31));
-                    if (none || alone) {
-                        rv[p][z] = Words<VN>{};
-                        rvs[p][z] = 0;
-                    }
+            for (int z = 0; z < 4; ++z) {
+                const int key = 4 * sq4 + z;
+                const bool none = t + key < t_lo || t + key >= t_hi;
+                const bool alone = !none && may_be_nonfinite<FMT, DT>(rv[z], rvs[z]);
+                if (alone) atomicOr(&s_apart[slot][key >> 5], 1u << (key & 31));
+                if (none || alone) {
+                    rv[z] = Words<VN>{};
+                    rvs[z] = 0;
                 }
             }
-            // a quad of keys in its group of 16: quads 0, 2, 1, 3
-            const int half = (quad & 3) >> 1, ch = (quad >> 2) * 2 + (quad & 1);
-            float s[4];
+        }
+        // (in a group of 16 keys the quads lie 0, 2, 1, 3)
+        const uint32_t to = place_of(to_v, slot);
+        float s[4];
 #pragma unroll
-            for (int z = 0; z < 4; ++z) s[z] = e8m0(rvs[p][z]);
+        for (int z = 0; z < 4; ++z) s[z] = e8m0(rvs[z]);
 #pragma unroll
-            for (int q = 0; q < VC / 2; ++q) {
-                uint32_t w[4];
+        for (int q = 0; q < VC / 2; ++q) {
+            uint32_t w[4];
 #pragma unroll
-                for (int z = 0; z < 4; ++z) w[z] = pair_of<FMT, DT>(rv[p][z], q, s[z]);
+            for (int z = 0; z < 4; ++z) w[z] = pair_of<FMT, DT>(rv[z], q, s[z]);
 #pragma unroll
-                for (int odd = 0; odd < 2; ++odd) {
-                    const uint32_t sel = odd ? 0x07060302u : 0x05040100u;
-                    reinterpret_cast<uint2 *>(s_v)[2 * (slot * SLOT + value_chunk<D, KT>(sn * VC + 2 * q + odd, ch)) + half] =
-                        make_uint2(__builtin_amdgcn_perm(w[1], w[0], sel), __builtin_amdgcn_perm(w[3], w[2], sel));
-                }
+            for (int odd = 0; odd < 2; ++odd) {
+                const int c = 2 * q + odd, x = KT == 128 ? c : c >> 1;
+                const uint32_t sel = odd ? 0x07060302u : 0x05040100u;
+                *reinterpret_cast<uint2 *>(lds + (to ^ 16 * x) + c * VROW) =
+                    make_uint2(__builtin_amdgcn_perm(w[1], w[0], sel), __builtin_amdgcn_perm(w[3], w[2], sel));
             }
         }
     };
@@ -275,22 +268,20 @@ __global__ __launch_bounds__(64 * NW, D < 256 ? 2 : 1) void kv_tile_kernel(const
     // Scores of 32 keys, their largest, the weights, the weighted values.
     struct Weights { u4v p[2]; };
     // Operands: chunk 2 s + hh of key 32 sub + n32, chunk 4 sub + 2 u + hh of
-    // channel 32 j + n32.  The lane's part of the exchange and of the row is in
-    // the base; s, sub, u and j exchange further, by constants.
-    constexpr int KROW = D * 2, VROW = KT * 2;
-    const uint32_t at_k = 16 * key_chunk<D>(n32, hh), at_v = 16 * (2 * SLOT + value_chunk<D, KT>(n32, hh));
-    const uint8_t *const lds = reinterpret_cast<const uint8_t *>(s_kv);
+    // channel 32 j + n32.
+    const uint32_t at_k = 16 * key_chunk<D>(n32, hh), at_v = 2 * SLOTB + 16 * value_chunk<D, KT>(n32, hh);
     const auto read_keys = [&](uint4 (&f)[S], int slot, int sub, int from, int to) SQ_INLINE {
+        const uint32_t at = place_of(at_k, slot);
 #pragma unroll
         for (int s = from; s < to; ++s)
-            f[s] = *reinterpret_cast<const uint4 *>(lds + ((at_k ^ 32 * (s & 7)) + slot * (SLOT * 16)) +
-                                                    sub * 32 * KROW + (s & ~7) * 32);
+            f[s] = *reinterpret_cast<const uint4 *>(lds + (at ^ 32 * (s & 7)) + sub * 32 * KROW + (s & ~7) * 32);
     };
     const auto read_values = [&](uint4 (&f)[JT], int slot, int sub, int u) SQ_INLINE {
+        const uint32_t at = place_of(at_v, slot);
 #pragma unroll
         for (int j = 0; j < JT; ++j) {
             const int x = (4 * sub + 2 * u ^ value_exchange<D, KT>(32 * j)) & (KT / 8 - 1);
-            f[j] = *reinterpret_cast<const uint4 *>(lds + ((at_v ^ 16 * x) + slot * (SLOT * 16)) + j * 32 * VROW);
+            f[j] = *reinterpret_cast<const uint4 *>(lds + (at ^ 16 * x) + j * 32 * VROW);
         }
     };
     const auto multiply_keys = [&](f32x16 &x, const uint4 (&f)[S]) SQ_INLINE {
@@ -377,8 +368,8 @@ __global__ __launch_bounds__(64 * NW, D < 256 ? 2 : 1) void kv_tile_kernel(const
 
     if (tid < 2 * UNITS) s_apart[tid / UNITS][tid % UNITS] = 0;
     if (n_tiles > 0) {
-        look_up_keys(0);
-        look_up_values(0);
+        page_k = page_of(tile_at(0) + sk);
+        page_v = page_of(tile_at(0) + 4 * sq4);
         load_keys(0);
         load_values(0);
         __syncthreads();  // (s_apart)
@@ -509,8 +500,9 @@ __global__ __launch_bounds__(256) void kv_tile_join_kernel(const KvAttention a, 
 
 template <int D, int FMT, int DT, int NW>
 static void launch_tile(const KvAttention &a, int rows_min, int splits, float *parts, hipStream_t stream) {
-    const int64_t tiles = a.T * a.group / (32 * NW) + (a.B < a.T ? a.B : a.T);
-    kv_tile_kernel<D, FMT, DT, NW><<<dim3((unsigned)(tiles * a.cache.heads), splits), 64 * NW, 0, stream>>>(
+    // (whatever the sequences' lengths: each leaves its last tile open at the most)
+    const int64_t open = a.B < a.T ? a.B : a.T, tiles = (a.T * a.group + open * (32 * NW - 1)) / (32 * NW);
+    kv_tile_kernel<D, FMT, DT, NW><<<(unsigned)(tiles * a.cache.heads * splits), 64 * NW, 0, stream>>>(
         a, rows_min, splits, parts, a.table);
     if (splits > 1) {
         const int64_t rows = a.T * a.q_heads, per = 256 / (D / 4);
@@ -521,7 +513,7 @@ static void launch_tile(const KvAttention &a, int rows_min, int splits, float *p
 template <int D, int FMT, int DT>
 static void launch_tile_nw(const KvAttention &a, int waves, int rows_min, int splits, float *parts,
                            hipStream_t stream) {
-    if constexpr (D < 256) {
+    if constexpr (D == 128) {
         if (waves == 8) return launch_tile<D, FMT, DT, 8>(a, rows_min, splits, parts, stream);
     }
     launch_tile<D, FMT, DT, 4>(a, rows_min, splits, parts, stream);
