@@ -65,14 +65,15 @@ __global__ __launch_bounds__(256, (blocks_per_cu(D, FMT, NT))) void kv_attn_kern
     const KvAttention a, int rows_max, const int32_t *__restrict__ tables) {
     using L = Tile32<D, FMT>;
     constexpr int NB = L::NB, RB = L::RB, J = D / 16;  // blocks, code bytes of a row; channel tiles
-    constexpr int kRing = 4 * L::stages * L::bytes, kJoin = 2 * NT * J * 64 * 16;
+    constexpr int kRing = 4 * L::stages * L::bytes, kJoin = 4 * NT * J * 64 * 16;
     __shared__ int s_at[2];
+    __shared__ KvSeq s_seq;
     __shared__ float s_m[4][16 * NT], s_l[4][16 * NT];
     // first the sequences' units, then the waves' rings, and (an item's keys
     // read) the join of the waves' sums
     __shared__ __attribute__((aligned(1024))) uint8_t s_ring[kRing > kJoin ? kRing : kJoin];
     int64_t *const s_pre = reinterpret_cast<int64_t *>(s_ring), *const s_wave = s_pre + 257;
-    const auto s_o = reinterpret_cast<f32x4(*)[NT * J][64]>(s_ring);
+    const auto s_o = reinterpret_cast<float(*)[64]>(s_ring);
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -124,18 +125,20 @@ __global__ __launch_bounds__(256, (blocks_per_cu(D, FMT, NT))) void kv_attn_kern
     if (s_pre[tid] * heads <= u0 && u0 < s_pre[tid + 1] * heads) {
         int64_t before = s_pre[tid] * heads;
         int b = b_first;
+        KvSeq s = kv_seq(a, b);
         for (;;) {
-            const int64_t n = (int64_t)units_of(kv_seq(a, b)) * heads;
+            const int64_t n = (int64_t)units_of(s) * heads;
             if (u0 < before + n) break;
             before += n;
-            ++b;
+            s = kv_seq(a, ++b);
         }
         s_at[0] = b;
         s_at[1] = (int)(u0 - before);
+        s_seq = s;
     }
     __syncthreads();
     int b = __builtin_amdgcn_readfirstlane(s_at[0]);
-    KvSeq seq = kv_seq(a, b);
+    KvSeq seq = s_seq;
     int units = units_of(seq);
     const int rem = __builtin_amdgcn_readfirstlane(s_at[1]);
     int h = __builtin_amdgcn_readfirstlane(rem / units);
@@ -403,8 +406,8 @@ __global__ __launch_bounds__(256, (blocks_per_cu(D, FMT, NT))) void kv_attn_kern
             }
         }
 
-        // Join the waves: one maximum, then the values of waves 2 and 3 into 0
-        // and 1, of 1 into 0.  (All loads to the rings have been waited for.)
+        // Join the waves: one maximum; the values through LDS, a quarter of the
+        // channels a wave.  (All loads to the rings have been waited for.)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             l[nt] += __shfl_xor(l[nt], 16, 64);
@@ -426,61 +429,51 @@ __global__ __launch_bounds__(256, (blocks_per_cu(D, FMT, NT))) void kv_attn_kern
             const float f = __builtin_amdgcn_exp2f(m[nt] - mx[nt]);
 #pragma unroll
             for (int j = 0; j < J; ++j) {
-                o[nt][j] *= f;
-                if (wave >= 2) s_o[wave - 2][nt * J + j][lane] = o[nt][j];
+                const f32x4 v = o[nt][j] * f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s_o[((wave * 4 + i) * NT + nt) * J + j][lane] = v[i];
             }
         }
         __syncthreads();
-        if (wave < 2) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int j = 0; j < J; ++j) {
-                    o[nt][j] += s_o[wave][nt * J + j][lane];
-                    if (wave == 1) s_o[1][nt * J + j][lane] = o[nt][j];
-                }
-        }
-        __syncthreads();
         const bool whole = count == units;
-        if (wave == 0) {
-            // a lane's values are D / 4 successive channels of its row
+        {
+            // value `wave` of a lane's four: J successive channels of its row
             const int slot = tile > 0 ? 0 : 1;
             float *const out = parts + (int64_t)(blockIdx.x * 2 + slot) * PartSize<D, NT>::floats;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 const int r = nt * 16 + n16;
-                float v[D / 4];
+                float v[J];
 #pragma unroll
                 for (int j = 0; j < J; ++j) {
-                    const f32x4 x = o[nt][j] + s_o[1][nt * J + j][lane];
+                    v[j] = 0.0f;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) v[i * J + j] = x[i];
+                    for (int w = 0; w < 4; ++w) v[j] += s_o[((w * 4 + wave) * NT + nt) * J + j][lane];
                 }
                 if (r < rows) {
+                    const int d = J * (4 * g + wave);
                     if (whole) {
                         const float inv = row_factor(sum[nt], seq.over);
                         const int i = r / group;
-                        uint4 *y = reinterpret_cast<uint4 *>(a.y) +
-                                   (((int64_t)(seq.q0 + i) * a.q_heads + h * group + r - i * group) * D + g * (D / 4)) / 8;
+                        uint2 *y = reinterpret_cast<uint2 *>(a.y) +
+                                   (((int64_t)(seq.q0 + i) * a.q_heads + h * group + r - i * group) * D + d) / 4;
 #pragma unroll
-                        for (int k = 0; k < D / 32; ++k)
-                            y[k] = make_uint4(pack16<DT>(v[8 * k] * inv, v[8 * k + 1] * inv),
-                                              pack16<DT>(v[8 * k + 2] * inv, v[8 * k + 3] * inv),
-                                              pack16<DT>(v[8 * k + 4] * inv, v[8 * k + 5] * inv),
-                                              pack16<DT>(v[8 * k + 6] * inv, v[8 * k + 7] * inv));
+                        for (int k = 0; k < J / 4; ++k)
+                            y[k] = make_uint2(pack16<DT>(v[4 * k] * inv, v[4 * k + 1] * inv),
+                                              pack16<DT>(v[4 * k + 2] * inv, v[4 * k + 3] * inv));
                     } else {
-                        float4 *y = reinterpret_cast<float4 *>(out + r * D + g * (D / 4));
+                        float4 *y = reinterpret_cast<float4 *>(out + r * D + d);
 #pragma unroll
-                        for (int k = 0; k < D / 16; ++k)
+                        for (int k = 0; k < J / 4; ++k)
                             y[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-                        if (g == 0) {
+                        if (g == 0 && wave == 0) {
                             out[16 * NT * D + r] = mx[nt];
                             out[16 * NT * D + 16 * NT + r] = sum[nt];
                         }
                     }
                 }
             }
-            if (lane == 0 && !whole && tile == 0) {
+            if (tid == 0 && !whole && tile == 0) {
                 Part p;
                 p.b = b;
                 p.h = h;
@@ -503,57 +496,75 @@ __global__ __launch_bounds__(256, (blocks_per_cu(D, FMT, NT))) void kv_attn_kern
     }
 }
 
-// Joins the parts of the item that block blockIdx.x began and did not end, one
-// row a block: 256 threads are D / 4 channel quads by as many of the parts at a
-// time.
+// Joins the parts of the item that block blockIdx.x began and did not end, a
+// row a time: 256 threads are D / 4 channel quads by W of the parts at a time.
+// All that a row's first W kAhead parts hold is asked for at once, before the
+// maximum is known: the kernel is a chain of memory latencies.
 template <int D, int DT, int NT>
 __global__ __launch_bounds__(256) void kv_join_kernel(const KvAttention a) {
-    constexpr int Q = D / 4, W = 256 / Q;
+    constexpr int Q = D / 4, W = 256 / Q, kAhead = 4, kRows = 16 * NT;
     const float *const work = reinterpret_cast<const float *>(a.work);
     const Part p = reinterpret_cast<const Part *>(work)[blockIdx.x];
-    const int r = blockIdx.y;
-    if (p.last < 0 || r >= p.rows) return;
+    if (p.last < 0) return;
     const float *const parts = work + kMaxBlocks * sizeof(Part) / sizeof(float);
     __shared__ f32x4 s_o[W][Q];
     __shared__ float s_f[kMaxBlocks], s_red[4];
-    const int d4 = threadIdx.x % Q, w = threadIdx.x / Q;
+    const int tid = threadIdx.x, d4 = tid % Q, w = tid / Q;
     const int first = blockIdx.x, n = p.last - first + 1;
+    const KvSeq seq = kv_seq(a, p.b);
     // (the first block's part is its second: it begins the item)
-    const auto part = [&](int i) SQ_INLINE { return parts + (int64_t)((first + i) * 2 + (i == 0)) * PartSize<D, NT>::floats; };
+    const auto part = [&](int i) SQ_INLINE {
+        return parts + (int64_t)((first + i) * 2 + (i == 0)) * PartSize<D, NT>::floats;
+    };
     const auto reduced = [&](float v, auto op) SQ_INLINE {
 #pragma unroll
         for (int off = 32; off; off >>= 1) v = op(v, __shfl_xor(v, off, 64));
-        if ((threadIdx.x & 63) == 0) s_red[threadIdx.x >> 6] = v;
+        if ((tid & 63) == 0) s_red[tid >> 6] = v;
         __syncthreads();
         v = op(op(s_red[0], s_red[1]), op(s_red[2], s_red[3]));
         __syncthreads();
         return v;
     };
-    float mx = kNoMax, sum = 0.0f;
-    for (int i = threadIdx.x; i < n; i += 256) {
-        s_f[i] = part(i)[16 * NT * D + r];
-        mx = fmaxf(mx, s_f[i]);
+    for (int r = blockIdx.y; r < p.rows; r += gridDim.y) {
+        f32x4 ahead[kAhead];
+#pragma unroll
+        for (int z = 0; z < kAhead; ++z) {
+            const int i = w + z * W;
+            ahead[z] = *reinterpret_cast<const f32x4 *>(part(i < n ? i : n - 1) + r * D + 4 * d4);
+        }
+        float mx = kNoMax, sum = 0.0f;
+        for (int i = tid; i < n; i += 256) {
+            s_f[i] = part(i)[kRows * D + r];
+            mx = fmaxf(mx, s_f[i]);
+        }
+        float l = tid < n ? part(tid)[kRows * D + kRows + r] : 0.0f;
+        mx = reduced(mx, [](float x, float y) { return fmaxf(x, y); });
+        for (int i = tid; i < n; i += 256) {
+            s_f[i] = __builtin_amdgcn_exp2f(s_f[i] - mx);
+            if (i >= 256) l = part(i)[kRows * D + kRows + r];
+            sum += l * s_f[i];
+        }
+        sum = reduced(sum, [](float x, float y) { return x + y; });
+        f32x4 o = {0, 0, 0, 0};
+#pragma unroll
+        for (int z = 0; z < kAhead; ++z)
+            if (w + z * W < n) o += ahead[z] * s_f[w + z * W];
+#pragma unroll 4
+        for (int i = w + kAhead * W; i < n; i += W)
+            o += *reinterpret_cast<const f32x4 *>(part(i) + r * D + 4 * d4) * s_f[i];
+        s_o[w][d4] = o;
+        __syncthreads();
+        if (w == 0) {
+            f32x4 v = o;
+            for (int i = 1; i < W; ++i) v += s_o[i][d4];
+            const float inv = row_factor(sum, seq.over);
+            const int i = r / a.group;
+            uint2 *y = reinterpret_cast<uint2 *>(a.y) +
+                       (((int64_t)(seq.q0 + i) * a.q_heads + p.h * a.group + r - i * a.group) * D + 4 * d4) / 4;
+            *y = make_uint2(pack16<DT>(v[0] * inv, v[1] * inv), pack16<DT>(v[2] * inv, v[3] * inv));
+        }
+        // (s_o and s_f are written again behind two barriers)
     }
-    mx = reduced(mx, [](float x, float y) { return fmaxf(x, y); });
-    for (int i = threadIdx.x; i < n; i += 256) {
-        s_f[i] = __builtin_amdgcn_exp2f(s_f[i] - mx);
-        sum += part(i)[16 * NT * D + 16 * NT + r] * s_f[i];
-    }
-    sum = reduced(sum, [](float x, float y) { return x + y; });
-    f32x4 o = {0, 0, 0, 0};
-#pragma unroll 8
-    for (int i = w; i < n; i += W) o += *reinterpret_cast<const f32x4 *>(part(i) + r * D + 4 * d4) * s_f[i];
-    s_o[w][d4] = o;
-    __syncthreads();
-    if (w != 0) return;
-    f32x4 v = o;
-    for (int i = 1; i < W; ++i) v += s_o[i][d4];
-    const KvSeq seq = kv_seq(a, p.b);
-    const float inv = row_factor(sum, seq.over);
-    const int i = r / a.group;
-    uint2 *y = reinterpret_cast<uint2 *>(a.y) +
-               (((int64_t)(seq.q0 + i) * a.q_heads + p.h * a.group + r - i * a.group) * D + 4 * d4) / 4;
-    *y = make_uint2(pack16<DT>(v[0] * inv, v[1] * inv), pack16<DT>(v[2] * inv, v[3] * inv));
 }
 
 // Which kernels a call takes.
@@ -606,7 +617,8 @@ template <int D, int FMT, int DT, int NT>
 static void launch_attn(const KvAttention &a, const Plan &p, hipStream_t stream) {
     kv_attn_kernel<D, FMT, DT, NT><<<(unsigned)p.blocks, 256, 0, stream>>>(a, p.rows_max, a.table);
     if (p.blocks > 1)
-        kv_join_kernel<D, DT, NT><<<dim3((unsigned)p.blocks, p.rows_max), 256, 0, stream>>>(a);
+        // (a block a row; beside the tile kernel most blocks have nothing to join)
+        kv_join_kernel<D, DT, NT><<<dim3((unsigned)p.blocks, p.waves ? 1 : p.rows_max), 256, 0, stream>>>(a);
 }
 
 template <int D, int FMT, int DT>
