@@ -52,12 +52,12 @@ template <int D, int FMT> struct Tile32 {
     static constexpr int stages = bytes < 4096 ? 4 : bytes < 8192 ? 3 : 2;
 };
 constexpr int kCus = 256;
-// Blocks of the kernel on a CU: LDS allows 3, 2 or 1 of them; with two column
-// groups registers allow 2, of 256 channels 1.
+// Blocks of the kernel on a CU: LDS allows 3, 2 or 1 of them, registers 2 with
+// two column groups.
 constexpr int blocks_per_cu(int dim, int fmt, int nt) {
     const int row = fmt == E2M1 ? dim / 2 : dim;  // code bytes: 32 to 256
     const int n = row <= 64 ? 3 : row <= 128 ? 2 : 1;
-    return nt == 1 ? n : dim == 256 ? 1 : n < 2 ? n : 2;
+    return nt == 1 || n < 2 ? n : 2;
 }
 
 template <int D, int FMT, int DT, int NT>
@@ -582,9 +582,11 @@ static Plan plan_attention(int64_t T, int q_heads, int heads, int dim, int fmt, 
                            int64_t max_q) {
     Plan p = {};
     const int64_t group = q_heads / heads, most = max_q * group;
-    // Up to 32 rows the first kernel has all. Of a call with longer sequences it
-    // takes those of up to 16 rows (or of one query), the tile kernel the others.
-    p.nt = most <= 16 ? 1 : most <= 32 ? 2 : group <= 16 ? 1 : group <= 32 ? 2 : 0;
+    // Up to 32 rows (16 with 256 channels: registers) the first kernel has all.
+    // Of a call with longer sequences it takes those of up to 16 rows (or of one
+    // query), the tile kernel the others.
+    const int two = dim == 256 ? 0 : 2;
+    p.nt = most <= 16 ? 1 : most <= 32 && two ? two : group <= 16 ? 1 : group <= 32 ? two : 0;
     p.rows_max = (int)(most < 16 * p.nt ? most : 16 * p.nt);
     if (p.nt) {
         const int64_t units = (int64_t)B * heads * ((keys + 15 + kTile - 1) / kTile);
@@ -592,7 +594,7 @@ static Plan plan_attention(int64_t T, int q_heads, int heads, int dim, int fmt, 
         p.blocks = units < most_blocks ? (units > 0 ? units : 1) : most_blocks;
         p.bytes = kMaxBlocks * sizeof(Part) + (size_t)p.blocks * 2 * 16 * p.nt * (dim + 2) * sizeof(float);
     }
-    if (most > 32) {
+    if (most > 16 * p.nt) {
         p.waves = dim != 128 || most <= 128 ? 4 : 8;
         // Blocks that the GPU holds at once (kv_attn_tile.hip: registers allow two
         // waves a SIMD, three of 64 channels, one of 256).  Where there are less
@@ -623,8 +625,10 @@ static void launch_attn(const KvAttention &a, const Plan &p, hipStream_t stream)
 
 template <int D, int FMT, int DT>
 static void launch_attn_nt(const KvAttention &a, const Plan &p, hipStream_t stream) {
-    if (p.nt == 1) launch_attn<D, FMT, DT, 1>(a, p, stream);
-    else launch_attn<D, FMT, DT, 2>(a, p, stream);
+    if constexpr (D < 256) {
+        if (p.nt == 2) return launch_attn<D, FMT, DT, 2>(a, p, stream);
+    }
+    launch_attn<D, FMT, DT, 1>(a, p, stream);
 }
 
 template <int D>
