@@ -113,8 +113,9 @@ int sq_dequantize_kv_mx(const sq_kv_cache *cache, const int32_t *table, int64_t 
  * as 0.  An infinity or NaN of a key or value reaches the queries that
  * see it and no others.  The same call gives the same bits every time; a
  * sequence's bits may depend on the others of the call.
- * q_heads % heads == 0, q_heads <= 65535, T and B * heads <= 2^24, T * q_heads
- * < 2^31, width * page < 2^31, finite scale, max_q >= 1 where T, B > 0.  T == 0
+ * q_heads % heads == 0, q_heads <= 65535, T <= 2^24, T * q_heads <= 2^29,
+ * B * heads <= 2^22, width * page <= 2^30, width * page / 128 * heads <= 2^30
+ * (SQ_ERR_UNSUPPORTED above), finite scale, max_q >= 1 where T, B > 0.  T == 0
  * or B == 0 enqueues nothing.
  */
 int sq_attention_kv_mx(const void *q, const int64_t q_stride[2], int dt, int64_t T,

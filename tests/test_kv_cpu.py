@@ -111,8 +111,9 @@ def test_attention_refuses():
     for kw, status in [(dict(dt=sq.SQ_F32), DTYPE), (dict(T=-1), SHAPE), (dict(q_heads=7), SHAPE),
                        (dict(q_heads=0), SHAPE), (dict(T=5), SHAPE), (dict(max_q=0), SHAPE),
                        (dict(max_q=-1), SHAPE), (dict(width=1 << 28), UNSUP),
-                       (dict(T=1 << 25, B=1 << 25), UNSUP), (dict(B=(1 << 23) + 1, T=(1 << 23) + 1), UNSUP),
-                       (dict(q_heads=65536), UNSUP), (dict(T=1 << 20, q_heads=2048, cu=FAKE), UNSUP),
+                       (dict(T=1 << 25, B=1 << 25), UNSUP),
+                       (dict(q_heads=65536), UNSUP), (dict(T=1 << 20, q_heads=1024, cu=FAKE), UNSUP),
+                       (dict(B=(1 << 21) + 1, T=(1 << 21) + 1), UNSUP), (dict(width=(1 << 26) + 1), UNSUP),
                        (dict(scale=math.inf), ARG), (dict(window=-1), ARG), (dict(q=None), NULL),
                        (dict(qs=None), NULL), (dict(lens=None), NULL), (dict(y=None), NULL),
                        (dict(table=None), NULL), (dict(ws=None), WORKSPACE), (dict(size=64), WORKSPACE),
@@ -122,6 +123,7 @@ def test_attention_refuses():
         assert call(**kw) == status, kw
     assert call(T=0, B=0, q=None, y=None, ws=None) == OK
     assert call(B=0, cu=FAKE) == OK
+    assert call(cache(heads=65535), width=1 << 24, q_heads=65535) == UNSUP
 
 
 @built
@@ -135,6 +137,8 @@ def test_workspace_sizes():
     assert size(1, 16, 1, 4096, 9) == one  # (one query is there)
     assert size(64, 16, 64, 4096, 1) == one
     assert size(7, 15, 7, 8, 1) == 0 and size(7, 16, 7, 8, 1, dim=96) == 0 and size(0, 16, 7, 8, 1) == 0
+    # 48 heads share a key's head: tiles, and none of them split where they are many
+    assert size(4096, 96, 4096, 64, 1) == 0 < size(40, 96, 40, 64, 1)
     # a prompt whose keys are split keeps its rows' parts for every split
     assert size(64, 16, 1, 4096, 64) >= 64 * 16 * 130 * 4 * 2
 

@@ -844,6 +844,8 @@ def rope_quantize_kv_mx(q, k, v, slots, cache, fmt=SQ_MX_E2M1, positions=None, i
         qp = q.data_ptr()
         y = _kv_result(out, "out", (T, q_heads, dim), dt, q.device, stream)
         yp = y.data_ptr()
+        if yp == qp and T:
+            raise ValueError("out is q: a rotation in place is not supported")
     elif q_mul is not None or out is not None:
         raise ValueError("q_mul and out need q")
     qm, km = _kv_mul(q_mul, "q_mul", q_heads, dim), _kv_mul(k_mul, "k_mul", heads, dim)
@@ -927,6 +929,8 @@ def attention_kv_mx(q, cache, table, seq_lens, cu_q=None, fmt=SQ_MX_E2M1, max_q=
     if window < 0:
         raise ValueError(f"window {window}")
     y = _kv_result(out, "out", (T, q_heads, dim), q.dtype, q.device, stream)
+    if y.data_ptr() == q.data_ptr() and T:
+        raise ValueError("out is q")
     need = lib().sq_attention_kv_mx_workspace(T, q_heads, c, B, width, max_q)
     if workspace is None:
         workspace = _mx_empty(1, need, torch.uint8, q.device, stream)

@@ -16,7 +16,8 @@ inline bool valid_dt(int dt) { return dt == SQ_F32 || dt == SQ_F16 || dt == SQ_B
 inline hipStream_t st(void *s) { return reinterpret_cast<hipStream_t>(s); }
 int finish() { return hipGetLastError() == hipSuccess ? SQ_OK : SQ_ERR_HIP; }
 
-constexpr int64_t kMaxTokens = 1 << 24, kMaxHeads = 65535, kMaxSlots = 0x7fffffff;
+constexpr int64_t kMaxTokens = 1 << 24, kMaxHeads = 65535, kMaxSlots = 0x7fffffff,
+                  kMaxKeys = 1 << 30;
 
 inline bool power_of_two(int64_t v) { return v > 0 && (v & (v - 1)) == 0; }
 
@@ -63,8 +64,11 @@ int check_attention(int64_t T, int64_t q_heads, const sq::KvCache &c, int64_t B,
     if (T < 0 || B < 0 || width < 0 || max_q < 0 || q_heads < 1) return SQ_ERR_SHAPE;
     if (q_heads % c.heads) return SQ_ERR_SHAPE;
     if (q_heads > kMaxHeads || T > kMaxTokens || B > kMaxTokens) return SQ_ERR_UNSUPPORTED;
-    if (T * q_heads > kMaxSlots || B * c.heads > kMaxTokens) return SQ_ERR_UNSUPPORTED;
-    if (width > kMaxSlots >> c.page_log) return SQ_ERR_UNSUPPORTED;
+    // (grids of fewer than 2^32 threads; keys, and tiles of keys of a sequence's
+    // heads, counted in 31 bits)
+    if (T * q_heads > (int64_t)1 << 29 || B * c.heads > (int64_t)1 << 22) return SQ_ERR_UNSUPPORTED;
+    if (width > kMaxKeys >> c.page_log) return SQ_ERR_UNSUPPORTED;
+    if (((width << c.page_log) >> 7) * c.heads > kMaxKeys) return SQ_ERR_UNSUPPORTED;
     return SQ_OK;
 }
 
@@ -179,7 +183,7 @@ int sq_attention_kv_mx(const void *q, const int64_t q_stride[2], int dt, int64_t
     const int64_t most = cu_q ? most_queries(max_q, T) : 1;
     const size_t need = sq::kv_attention_workspace(T, (int)q_heads, a.cache.heads, a.cache.dim, a.cache.fmt, (int)B,
                                                    width << a.cache.page_log, most);
-    if (!workspace || workspace_bytes < need) return SQ_ERR_WORKSPACE;
+    if (need && (!workspace || workspace_bytes < need)) return SQ_ERR_WORKSPACE;
     if (!aligned(workspace, 16)) return SQ_ERR_ALIGN;
     a.q = q;
     a.q_st = q_stride[0];
