@@ -92,10 +92,11 @@ int sq_dequantize_kv_mx(const sq_kv_cache *cache, const int32_t *table, int64_t 
  *   j <= p (causal != 0) or j < n_k (causal == 0), and
  *   j > p - window (window > 0)
  *   y = sum_j w_j v_j, w = softmax over those j of scale * (q . k_j)
- * A query that sees no key gets 0.  Query head h reads key head h / (q_heads /
+ * A query that sees no key gets 0, one that sees keys but scores all of them
+ * -inf NaN (0 / 0).  Query head h reads key head h / (q_heads /
  * heads).  Keys and values are the cache's, read in dt (round-to-nearest-even;
- * bf16 holds all but those of e4m3 blocks with e < 3; in fp16 magnitudes from
- * 65520 on become infinite).  Products are summed in fp32, the softmax's
+ * bf16 holds all in its range but those of e4m3 blocks with e < 3; in fp16
+ * magnitudes from 65520 on become infinite).  Products are summed in fp32, the softmax's
  * maximum and sum are fp32; its weights are rounded to dt for the product with
  * the values.
  *   q        [T, q_heads, dim] of dt (SQ_F16 or SQ_BF16), strides as above

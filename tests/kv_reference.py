@@ -32,10 +32,14 @@ def quantized(v, fmt):
 
 
 def values(q, e, fmt):
-    """float64 values [.., D] of codes and scale bytes (NaN where e is 255)."""
+    """float64 values [.., D] of codes and scale bytes (NaN where e is 255, or
+    an e4m3 code is a NaN)."""
     if e.size == 0:
         return np.zeros(e.shape[:-1] + (e.shape[-1] * 32,))
-    return mx.decode(q.reshape(-1, q.shape[-1]), e.reshape(-1, e.shape[-1]), fmt).reshape(*e.shape[:-1], -1)
+    nan = (q & 0x7f) == 0x7f if fmt == mx.E4M3 else np.zeros((), bool)
+    q = np.where(nan, 0, q).astype(np.uint8)
+    x = mx.decode(q.reshape(-1, q.shape[-1]), e.reshape(-1, e.shape[-1]), fmt).reshape(*e.shape[:-1], -1)
+    return np.where(nan, np.nan, x)
 
 
 class Cache:

@@ -99,6 +99,54 @@ def test_queries_that_are_not_finite_stay_alone(T):
     assert (np.abs(y - want)[rest] <= tol[rest]).all()
 
 
+@pytest.mark.parametrize("fmt", ["e2m1", "e4m3"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("T,n", [(1, 1), (1, 40), (1, 5000), (3, 200), (70, 90), (70, 5000), (70, 30)])
+def test_scores_of_minus_infinity(T, n, dim, fmt):
+    """Keys of -2^17 are infinite in fp16, their scores -inf: a query that sees
+    no others has a softmax of 0 / 0 and gets NaN, one that sees a finite key
+    too has all its weight there, one that sees no key gets 0."""
+    log(f"scores of -inf {T} {n} {dim} {fmt}")
+    rng = np.random.default_rng(26)
+    q = np.ones((T, 4, dim), np.float32)
+    k, v = (rng.standard_normal((n, 2, dim)).astype(np.float32) for _ in range(2))
+    k[:, :, 0], k[:, :, 1:32] = -2.0 ** 17, 0.0
+    f = {"e2m1": mx.E2M1, "e4m3": mx.E4M3}[fmt]
+    y, _, _ = _one(q, k, v, "f16", fmt=f)
+    blind = max(T - n, 0)  # queries before the first key
+    assert (y[:blind] == 0).all()
+    assert np.isnan(y[blind:]).all()
+    k[n - 1, :, 0] = 0.0
+    y, _, _ = _one(q, k, v, "f16", fmt=f)
+    assert (y[:blind] == 0).all()
+    assert np.isnan(y[blind:T - 1]).all()
+    last = ref.values(*ref.quantized(v[n - 1:], f), f)[0]  # (at most 8 bits, in fp16's range: exact)
+    assert (y[T - 1] == np.repeat(last, 2, axis=0)).all()
+
+
+@pytest.mark.parametrize("new", [(1, 1), (4, 3), (100, 90)])
+@pytest.mark.parametrize("which", ["key", "value"])
+@pytest.mark.parametrize("code", [0x7f, 0xff])
+def test_codes_that_are_nan(new, which, code):
+    """e4m3 codes of NaN, in the last token and among the queries' own."""
+    def mark(cache, q):
+        held = cache.kq if which == "key" else cache.vq
+        for b, t in ((0, cache.lens[0] - 1), (1, cache.lens[1] - 2)):
+            p, at = cache.where(b)
+            held[p[t], 0, at[t], 37] = code
+    run_attention(((300, 140), new, 4, 2, 64, 16, "f16", "e4m3", True, 0), mark)
+
+
+@pytest.mark.parametrize("new", [(1, 1, 1), (3, 5, 1), (90, 1, 77)])
+@pytest.mark.parametrize("fmt", ["e2m1", "e4m3"])
+def test_pages_that_sequences_share(new, fmt):
+    """Sequences with the same first pages, one of them twice in a row."""
+    def mark(cache, q):
+        cache.table[1, :6] = cache.table[0, :6]
+        cache.table[2, :4] = cache.table[0, 2]
+    run_attention(((300, 140, 200), new, 4, 2, 128, 16, "bf16", fmt, True, 0), mark)
+
+
 @pytest.mark.parametrize("T", [1, 3, 60])
 def test_windows_of_one_and_beyond_the_length(T):
     rng = np.random.default_rng(24)

@@ -453,8 +453,8 @@ __global__ __launch_bounds__(256, (blocks_per_cu(D, FMT, NT))) void kv_attn_kern
                 if (r < rows) {
                     const int d = J * (4 * g + wave);
                     if (whole) {
-                        const float inv = row_factor(sum[nt], seq.over);
                         const int i = r / group;
+                        const float inv = row_factor(sum[nt], r_hi[nt], seq.over);
                         uint2 *y = reinterpret_cast<uint2 *>(a.y) +
                                    (((int64_t)(seq.q0 + i) * a.q_heads + h * group + r - i * group) * D + d) / 4;
 #pragma unroll
@@ -557,8 +557,8 @@ __global__ __launch_bounds__(256) void kv_join_kernel(const KvAttention a) {
         if (w == 0) {
             f32x4 v = o;
             for (int i = 1; i < W; ++i) v += s_o[i][d4];
-            const float inv = row_factor(sum, seq.over);
             const int i = r / a.group;
+            const float inv = row_factor(sum, keys_end(a, seq, i), seq.over);
             uint2 *y = reinterpret_cast<uint2 *>(a.y) +
                        (((int64_t)(seq.q0 + i) * a.q_heads + p.h * a.group + r - i * a.group) * D + 4 * d4) / 4;
             *y = make_uint2(pack16<DT>(v[0] * inv, v[1] * inv), pack16<DT>(v[2] * inv, v[3] * inv));

@@ -133,12 +133,6 @@ struct KvSeq {
     bool over;  // longer than its row of the table: its queries get NaN
 };
 
-// What a row's weighted values are multiplied by: nothing seen gives 0.
-__device__ __forceinline__ float row_factor(float sum, bool over) {
-    if (over) return __uint_as_float(0x7fc00000u);
-    return sum == 0.0f ? 0.0f : 1.0f / sum;
-}
-
 __device__ __forceinline__ KvSeq kv_seq(const KvAttention &a, int b) {
     KvSeq s;
     const int T = (int)a.T;
@@ -159,6 +153,19 @@ __device__ __forceinline__ KvSeq kv_seq(const KvAttention &a, int b) {
     const int64_t lo = a.window ? (int64_t)s.nk - s.nq + 1 - a.window : 0;
     s.lo = lo > 0 ? (int)lo : 0;
     return s;
+}
+
+// The keys that a sequence's query i sees end here (none: 0 or less).
+__device__ __forceinline__ int keys_end(const KvAttention &a, const KvSeq &s, int i) {
+    return a.causal ? s.nk - s.nq + i + 1 : s.nk;
+}
+
+// What a row's weighted values are multiplied by, `end` its keys_end.  No key
+// seen gives 0; of a row that sees some, the weights sum to 0 only where every
+// score is -inf: 0 / 0.
+__device__ __forceinline__ float row_factor(float sum, int end, bool over) {
+    if (over || (end > 0 && sum == 0.0f)) return __uint_as_float(0x7fc00000u);
+    return end > 0 ? 1.0f / sum : 0.0f;
 }
 
 }  // namespace sq

@@ -444,7 +444,7 @@ __global__ __launch_bounds__(64 * NW, D == 64 ? 3 : D == 128 ? 2 : 1) void kv_ti
     if (row >= rows) return;
     const int64_t out = (int64_t)(seq.q0 + query) * a.q_heads + h * group + row - query * group;
     if (splits == 1) {
-        const float inv = row_factor(l, seq.over);
+        const float inv = row_factor(l, r_hi, seq.over);
         uint2 *y = reinterpret_cast<uint2 *>(a.y) + out * (D / 4) + hh;
 #pragma unroll
         for (int j = 0; j < JT; ++j)
@@ -493,7 +493,7 @@ __global__ __launch_bounds__(256) void kv_tile_join_kernel(const KvAttention a, 
         sum += s[(i * all + row) * 2 + 1] * e;
         v += *reinterpret_cast<const f32x4 *>(parts + (i * all + row) * D + 4 * d4) * e;
     }
-    const float inv = row_factor(sum, seq.over);
+    const float inv = row_factor(sum, keys_end(a, seq, t - seq.q0), seq.over);
     reinterpret_cast<uint2 *>(a.y)[row * Q + d4] =
         make_uint2(pack16<DT>(v[0] * inv, v[1] * inv), pack16<DT>(v[2] * inv, v[3] * inv));
 }
