@@ -901,8 +901,9 @@ def attention_kv_mx(q, cache, table, seq_lens, cu_q=None, fmt=SQ_MX_E2M1, max_q=
     (None: one query a sequence).  table int32 [B, width].  max_q: an upper
     bound of a sequence's queries (T without it).  scale: 1 / sqrt(dim) unless
     given.  window > 0: a query sees that many keys at the most, itself the
-    last.  A query that sees no key gets 0, one whose scores are all -inf NaN.  workspace: attention_kv_mx_workspace
-    bytes (uint8), used by this call alone while it runs; allocated without it."""
+    last.  A query that sees no key gets 0, one whose scores are all -inf NaN.
+    workspace: attention_kv_mx_workspace bytes (uint8), used by this call alone
+    while it runs; allocated without it."""
     c = _kv_cache(cache, fmt)
     dim = c.dim
     torch = _torch_mod

@@ -6,11 +6,12 @@
 // S^T = K Q^T (16 keys x 16 rows, 32 channels an instruction) and
 // O^T = V^T P^T (16 channels x 16 rows, 32 keys an instruction).  So laid out,
 // a lane holds scores of one row in S^T just where the second product takes
-// its weights, no lane exchanges data in the loop, and codes go from memory to
-// the operands through registers alone: a lane's key operand is successive
-// channels of one key (any order of the channels serves, the query's operand
-// having the same), a value operand eight keys of one channel, whose pairs are
-// joined by a byte permute after the conversion.
+// its weights, and no lane exchanges data in the loop.  Codes go from memory to
+// a ring of tiles in LDS, each wave's its own, by loads that take no registers,
+// and are converted as they are read from there: a lane's key operand is
+// successive channels of one key (any order of the channels serves, the query's
+// operand having the same), a value operand eight keys of one channel, whose
+// pairs are joined by a byte permute after the conversion.
 //
 // Memory bound, so the work is cut into equal shares whatever the sequences'
 // lengths: the tiles of 128 keys of all items in a row, a share of successive
@@ -18,6 +19,13 @@
 // across shares each block leaves its sum, maximum and weighted values in the
 // workspace (at most two parts a block: the item it continues and the one it
 // leaves off), and a second kernel joins them in the order of the blocks.
+//
+// 64 tokens over 130 .. 32768 keys, 64 / 8 heads of 128, e2m1: 86 us, 425 MB at
+// 4.9 TB/s (without the arithmetic, in a copy for timing, 74); with codes loaded
+// to registers it was 147.  A wave issues 252 vector, 107 scalar and 23 LDS
+// instructions for 32 keys, which fill 58 % of the vector units' cycles.  16
+// tokens over 900 .. 2300 keys, 56 heads of 128, e4m3: 63 us, 5.7 TB/s.  One
+// token over 2049 keys, 64 / 8 heads: 7.7 us and 4.1 of the joining kernel.
 #include "kv_attn_device.h"
 
 namespace sq {
@@ -582,9 +590,11 @@ static Plan plan_attention(int64_t T, int q_heads, int heads, int dim, int fmt, 
                            int64_t max_q) {
     Plan p = {};
     const int64_t group = q_heads / heads, most = max_q * group;
-    // Up to 32 rows (16 with 256 channels: registers) the first kernel has all.
-    // Of a call with longer sequences it takes those of up to 16 rows (or of one
-    // query), the tile kernel the others.
+    // Up to 32 rows (16 with 256 channels: registers) the first kernel has all:
+    // 24 rows over 4000 .. 8000 keys, 16 sequences of 4 heads of 128, take it
+    // 26 us, and the tile kernel 50 + 11 with 128 channels, 20 against 39 + 11
+    // with 64.  Of a call with longer sequences it takes those of up to 16 rows
+    // (or of one query), the tile kernel the others.
     const int two = dim == 256 ? 0 : 2;
     p.nt = most <= 16 ? 1 : most <= 32 && two ? two : group <= 16 ? 1 : group <= 32 ? two : 0;
     p.rows_max = (int)(most < 16 * p.nt ? most : 16 * p.nt);
@@ -595,10 +605,18 @@ static Plan plan_attention(int64_t T, int q_heads, int heads, int dim, int fmt, 
         p.bytes = kMaxBlocks * sizeof(Part) + (size_t)p.blocks * 2 * 16 * p.nt * (dim + 2) * sizeof(float);
     }
     if (most > 16 * p.nt) {
+        // With 128 channels eight waves share what a block converts where they
+        // have rows (a prompt of 8192, 64 / 8 heads: 1251 us, with four 1372; 256
+        // rows over 2000 .. 8000 keys: 76 and 78); up to 128 rows four waves do
+        // (128 rows: 46 us, with eight 71; 64 rows over 4000 keys: 27 and 31).
+        // With 64 channels four waves, three blocks a CU (windowed chunks of 77 ..
+        // 1013: 53 us, with eight 67; a prompt of 8192, 32 / 4 heads: 458 and 446);
+        // with 256 a wave takes all of a SIMD's registers.
         p.waves = dim != 128 || most <= 128 ? 4 : 8;
         // Blocks that the GPU holds at once (kv_attn_tile.hip: registers allow two
         // waves a SIMD, three of 64 channels, one of 256).  Where there are less
-        // than half of them, the keys of each tile are split over blocks.
+        // than half of them, the keys of each tile are split over blocks (64 tokens
+        // over 32768 keys, 64 / 8 heads: 85 us and 12 of the join, unsplit 882).
         const int64_t slots = kCus * (dim == 64 ? 3 : dim == 128 && p.waves == 4 ? 2 : 1);
         const int64_t tiles = (T * group + 32 * p.waves - 1) / (32 * p.waves) * heads;
         int64_t splits = slots / tiles;

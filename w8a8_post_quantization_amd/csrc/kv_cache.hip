@@ -153,6 +153,8 @@ static void launch_write_fmt(const RopeWrite &a, hipStream_t stream) {
     // pieces of 256 bytes of a token lie far apart in time)
     const Deal d = deal_rows(a.T, a.cache.dim, rows, 2);
     const dim3 grid((unsigned)d.groups, (unsigned)d.y);
+    // (past what the caches hold, data read once is kept out of them: 129 us for
+    // the 16384 tokens above, 135 without; 333 tokens either way 9)
     if (a.T * rows * a.cache.dim * dt_bytes(DT) > kNtLoadBytes)
         kv_write_kernel<DT, FMT, true><<<grid, 256, 0, stream>>>(a, d.tok_log);
     else
@@ -173,7 +175,8 @@ void launch_rope_write(const RopeWrite &a, int dt, hipStream_t stream) {
 
 // -------------------------------------------------------------- the way back
 
-// 62494 tokens of 8 heads of 128 from e2m1 to bf16 50 us: 324 MB at 6.5 TB/s.
+// Bound by memory: 62494 tokens of 8 heads of 128 from e2m1 to bf16 50 us, 324 MB
+// at 6.5 TB/s.
 
 // Two fp32 values of a byte of e2m1 codes, or of a half of e4m3 codes.
 template <int FMT>
@@ -263,6 +266,7 @@ static void launch_read_fmt(const KvRead &a, hipStream_t stream) {
     const int rows = 2 * a.cache.heads;
     const Deal d = deal_rows(a.total, a.cache.dim, rows, 5);
     const dim3 grid((unsigned)d.groups, (unsigned)d.y);
+    // (as above: 51 us for 62494 tokens, 63 without)
     if (a.total * rows * a.cache.dim * dt_bytes(DT) > kNtLoadBytes)
         kv_read_kernel<DT, FMT, true><<<grid, 256, 0, stream>>>(a, d.tok_log);
     else
