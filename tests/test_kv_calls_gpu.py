@@ -157,6 +157,21 @@ def test_windows_of_one_and_beyond_the_length(T):
         assert (np.abs(y - want) <= tol).all(), window
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("T,n", [(1, 1), (5, 1), (5, 150), (60, 1), (60, 0), (60, 150)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_the_largest_windows(T, n, dim, causal):
+    """Windows up to 2^63 - 1 hide nothing, with more queries than keys too."""
+    rng = np.random.default_rng(27)
+    q, k, v = (rng.standard_normal(s).astype(np.float32) for s in ((T, 2, dim), (n, 2, dim), (n, 2, dim)))
+    plain, want, tol = _one(q, k, v, "bf16", causal=causal)
+    assert (np.abs(plain - want) <= tol).all()
+    for window in (1 << 30, (1 << 30) + 1, 1 << 62, (1 << 63) - 1):
+        log(f"window {window} {T} {n} {dim} {causal}")
+        y, _, _ = _one(q, k, v, "bf16", causal=causal, window=window)
+        assert (y == plain).all(), window
+
+
 def test_heads_with_any_strides():
     """Queries laid out [heads, tokens, channels], keys from a wider row."""
     import torch

@@ -199,7 +199,8 @@ int sq_attention_kv_mx(const void *q, const int64_t q_stride[2], int dt, int64_t
     a.group = (int)(q_heads / a.cache.heads);
     a.scale = scale;
     a.causal = causal != 0;
-    a.window = window;
+    // (no sequence has as many keys: kernels count places less the window in 64 bits)
+    a.window = window > kMaxKeys ? 0 : window;
     a.work = workspace;
     sq::launch_kv_attention(a, most, dt, st(stream));
     return finish();
