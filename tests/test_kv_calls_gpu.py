@@ -172,6 +172,25 @@ def test_the_largest_windows(T, n, dim, causal):
         assert (y == plain).all(), window
 
 
+@pytest.mark.parametrize("T", [1, 40])
+@pytest.mark.parametrize("fmt", ["e2m1", "e4m3"])
+def test_keys_and_values_near_the_types_smallest(T, fmt):
+    """Keys of 2^-126 and 2^-124 in bf16 against queries of 2^126, keys and values of 2^-16
+    in fp16: what the codes stand for is subnormal in the type, and held."""
+    f = {"e2m1": mx.E2M1, "e4m3": mx.E4M3}[fmt]
+    for dt, key, value, query in (("bf16", -126 if f == mx.E2M1 else -124, 0, 126), ("f16", -16, -16, 12)):
+        log(f"small keys {dt} {T} {fmt}")
+        rng = np.random.default_rng(28)
+        q = np.ldexp(rng.uniform(-1, 1, (T, 4, 128)), query).astype(np.float32)
+        k = np.ldexp(rng.standard_normal((300, 2, 128)), key).astype(np.float32)
+        v = np.ldexp(rng.standard_normal((300, 2, 128)), value).astype(np.float32)
+        if f == mx.E4M3:  # (whole multiples of 1/32 of the size: in the type to the bit)
+            k = np.ldexp(np.rint(np.ldexp(k, 5 - key)), key - 5).astype(np.float32)
+            v = np.ldexp(np.rint(np.ldexp(v, 5 - value)), value - 5).astype(np.float32)
+        y, want, tol = _one(q, k, v, dt, scale=2.0 ** (-key - query - 3), fmt=f)
+        assert (np.abs(y - want) <= tol).all(), (dt, (np.abs(y - want) / tol).max())
+
+
 def test_heads_with_any_strides():
     """Queries laid out [heads, tokens, channels], keys from a wider row."""
     import torch
@@ -541,3 +560,15 @@ def test_the_binding_refuses():
     assert write(q=q[:0], k=k[:0], v=k[:0], slots=i64[:0]).shape == (0, 4, 64)
     assert att(q=q[:0], table=table[:0], seq_lens=n[:0]).shape == (0, 4, 64)
     assert read(total=0)[0].shape == (0, 2, 64)
+
+
+def test_the_binding_refuses_outputs_that_are_one():
+    import torch
+
+    c = sq.new_kv_cache_mx(4, 2, 16, 64)
+    k = torch.zeros(3, 2, 64, device="cuda", dtype=torch.float16)
+    with pytest.raises(sq.SQError):
+        sq.rope_quantize_kv_mx(None, k, k, torch.arange(3, device="cuda"), (c[0], c[1], c[0], c[1]))
+    with pytest.raises(sq.SQError):
+        sq.dequantize_kv_mx(c, torch.zeros(1, 1, dtype=torch.int32, device="cuda"),
+                            torch.tensor([0, 3], dtype=torch.int32, device="cuda"), 3, out=(k, k))

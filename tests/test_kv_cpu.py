@@ -127,6 +127,17 @@ def test_attention_refuses():
 
 
 @built
+def test_outputs_that_are_one_refuse():
+    """Keys and values that would be written over one another."""
+    L = sq.lib()
+    s = strides(1024, 128)
+    for kw in (dict(), dict(vq=FAKE + 64), dict(vs=FAKE + 64)):
+        assert L.sq_rope_quantize_kv_mx(None, None, FAKE, s, FAKE, s, sq.SQ_F16, 4, 0, None, None, 0, 1.0, 0, None,
+                                        None, FAKE, cache(**kw), None, None) == ARG, kw
+    assert L.sq_dequantize_kv_mx(cache(), FAKE, 2, 3, FAKE, 9, FAKE, FAKE, sq.SQ_BF16, None) == ARG
+
+
+@built
 def test_workspace_sizes():
     """Enough for the parts of the blocks, whatever the lengths: it depends on
     shapes alone, and refused shapes need none."""

@@ -105,6 +105,8 @@ int sq_rope_quantize_kv_mx(const void *q, const int64_t q_stride[2], const void 
     if (!slots || (rotary && (!positions || !inv_freq))) return SQ_ERR_NULL;
     if (!aligned(slots, 8) || !aligned(k_mul, 16) || !aligned(positions, 8) || !aligned(inv_freq, 8))
         return SQ_ERR_ALIGN;
+    // (keys and values would be written over one another)
+    if (cache->kq == cache->vq || cache->ks == cache->vs) return SQ_ERR_ARG;
     a.q = q;
     a.k = k;
     a.v = v;
@@ -142,6 +144,7 @@ int sq_dequantize_kv_mx(const sq_kv_cache *cache, const int32_t *table, int64_t 
     if (const int e = check_arrays(cache)) return e;
     if (!cu || !k || !v || (width && !table)) return SQ_ERR_NULL;
     if (!aligned(k, 16) || !aligned(v, 16) || !aligned(table, 4) || !aligned(cu, 4)) return SQ_ERR_ALIGN;
+    if (k == v) return SQ_ERR_ARG;  // (written over one another)
     a.table = table;
     a.width = width;
     a.cu = cu;
