@@ -21,7 +21,8 @@
  *
  * Alignment: all of q, k, v, y, kq, vq, their rows' strides in bytes, the
  * multipliers and the workspace 16 bytes; ks, vs 4 bytes; other arrays their
- * element size.  Inputs and outputs do not overlap.
+ * element size.  Inputs and outputs do not overlap,
+ * nor do outputs (the cache's keys and values, a call's k and v) one another.
  */
 #ifndef SQ_KV_H
 #define SQ_KV_H
