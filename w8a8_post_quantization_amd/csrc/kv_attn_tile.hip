@@ -395,6 +395,7 @@ __global__ __launch_bounds__(64 * NW, D == 64 ? 3 : D == 128 ? 2 : 1) void kv_ti
         wait_vmcnt<0>();  // (else the queries' loads count as pending in the loop)
         for (int i = 0; i < n_tiles; ++i) {
             const int t = tile_at(i), slot = i & 1;
+            uint32_t apart[UNITS];  // the tile's keys set apart
             // Unit u of the tile is weighted, the next one (whose keys' operands
             // are read) scored, and the operands of the one after it read.
             const auto unit = [&](auto number) SQ_INLINE {
@@ -426,11 +427,16 @@ __global__ __launch_bounds__(64 * NW, D == 64 ? 3 : D == 128 ? 2 : 1) void kv_ti
                 // the last reads of a slot and its staging.
                 if constexpr (u == 0 || u == (UNITS == 4 ? 2 : 1)) lds_barrier();
                 read_keys(kf, u + 2 < UNITS ? slot : slot ^ 1, (u + 2) % UNITS, 0, S / 2);
-                const uint32_t apart = __builtin_amdgcn_readfirstlane(s_apart[slot][u]);
+                // (all units' at once: between the tile's second barrier and the
+                // next one's first they are cleared)
+                if constexpr (u == 0) {
+#pragma unroll
+                    for (int z = 0; z < UNITS; ++z) apart[z] = __builtin_amdgcn_readfirstlane(s_apart[slot][z]);
+                }
                 multiply_values(w.p[1], vf[1]);
                 const float top = largest(x[~u & 1]);
-                if (apart) {
-                    add_apart(w, t + 32 * u, apart);
+                if (apart[u]) {
+                    add_apart(w, t + 32 * u, apart[u]);
                     // (loads of it that are left unused would be waited for below,
                     // whether it ran or not)
                     wait_vmcnt<0>();
