@@ -1,0 +1,61 @@
+"""The attention's softmax weights at the ends of their range: weights far below
+the largest, which fp16 holds with few bits or not at all."""
+import numpy as np
+import pytest
+
+import w8a8_post_quantization_amd as sq
+from tests import kv_reference as ref
+from tests import mx_reference as mx
+from tests.gpu_util import dev, log
+from tests.test_kv_gpu import FMTS, on_gpu, to_dt
+
+pytestmark = pytest.mark.gpu
+
+
+def attend(cache, q, dt, seqs, scale, window=0):
+    """q [T, heads, D] over the cache's one sequence, `seqs` times in a call:
+    float64 y of each."""
+    import torch
+
+    T = q.shape[0]
+    y = sq.attention_kv_mx(dev(np.tile(q, (seqs, 1, 1)), torch), on_gpu(torch, cache.arrays()),
+                           dev(np.repeat(cache.table, seqs, 0), torch),
+                           dev(np.full(seqs, cache.lens[0], np.int32), torch),
+                           dev(np.arange(seqs + 1, dtype=np.int32) * T, torch), fmt=cache.fmt, max_q=T, scale=scale,
+                           window=window)
+    torch.cuda.synchronize()
+    return y.double().cpu().numpy().reshape(seqs, *q.shape)
+
+
+@pytest.mark.parametrize("spread", [0.0, 0.4])
+@pytest.mark.parametrize("nats", [14.0, 16.0, 18.0])
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("T,seqs", [(1, 512), (3, 256), (40, 4), (150, 2)])
+@pytest.mark.parametrize("fmt,dim", [("e2m1", 128), ("e4m3", 64)])
+def test_small_weights_add_up(fmt, dim, T, seqs, dt, nats, spread):
+    """A first key whose score is 14 to 18 nats above some 3500 others, and whose
+    value is 0: the output is the others' alone.
+
+    The bound is that of ref.attention but for fp16's smallest step.  There a
+    weight is rounded by 2^-25 at the most where it is below 2^-14, and the
+    sequence's largest weight is 2^7 at least, so a key adds 2^-32 |v| and not
+    2^-25 |v| to the error."""
+    log(f"small weights {fmt} {dim} {T} {seqs} {dt} {nats} {spread}")
+    rng = np.random.default_rng(61)
+    n, scale = 3500, dim ** -0.5
+    d = np.sign(rng.standard_normal(dim)).astype(np.float32)
+    size = nats / (2.0 * dim * scale)  # the first key is 2 d
+    q = to_dt(np.broadcast_to(d * np.float32(size), (T, 1, dim)), dt)
+    k = (spread * rng.standard_normal((n, 1, dim))).astype(np.float32)
+    k[0, 0] = 2.0 * d
+    v = (64.0 + 32.0 * rng.random((n, 1, dim))).astype(np.float32)
+    v[0] = 0.0
+    cache = ref.Cache(rng, [n], 1, 64, dim, FMTS[fmt], k=[k], v=[v])
+    keys, values = cache.read(0)
+    want, tol = ref.attention(mx.to_f32(q).astype(np.float64), keys, values, dt, scale)
+    if dt == "f16":
+        seen = np.cumsum(np.abs(values), axis=0)[n - T:]  # [T, 1, D]: of each query's keys
+        tol = tol - (2.0 ** -25 - 2.0 ** -32) * seen
+    got = attend(cache, q, dt, seqs, scale)
+    err = np.abs(got - want)
+    assert (err <= tol).all(), (err / tol).max()

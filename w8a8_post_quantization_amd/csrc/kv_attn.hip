@@ -326,12 +326,11 @@ __global__ __launch_bounds__(256, (blocks_per_cu(D, FMT, NT))) void kv_attn_kern
                 }
 #pragma unroll
                 for (int i = 0; i < 8; ++i) top = fmaxf(top, x[nt][i]);
-                // The maximum may trail the true one by 8 (weights up to 256):
-                // rows are rescaled only where it is passed by more.
-                if (__any(top > m[nt] + 8.0f)) {
+                // Rows are rescaled only where the maximum trails by more than it may.
+                if (__any(top > m[nt] + (kTrail + kLift<DT>))) {
                     top = fmaxf(top, __shfl_xor(top, 16, 64));
                     top = fmaxf(top, __shfl_xor(top, 32, 64));
-                    const float mn = fmaxf(m[nt], top);
+                    const float mn = fmaxf(m[nt], top - kLift<DT>);
                     const float f = __builtin_amdgcn_exp2f(m[nt] - mn);
                     m[nt] = mn;
                     l[nt] *= f;

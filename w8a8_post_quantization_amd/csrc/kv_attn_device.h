@@ -17,6 +17,16 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 // key yet.
 constexpr float kNoMax = -3.402823466e38f;
 
+// Weights are 2^(score - m).  m is set to a row's largest score less kLift, and
+// may trail the true one by kTrail more before the row is rescaled: rescaling is
+// rare.  fp16 holds 2^-14 .. 2^15 in full and nothing below 2^-25, so its weights
+// are lifted to the upper end, 2^(kTrail + kLift) = 2^15 at the most: those of
+// 2^-21 of the largest have all their bits, those of 2^-32 are lost (unlifted,
+// 3500 keys of 2^-26 each, 18 nats below the first, came out up to 10 bounds
+// off).  bf16 has fp32's range.
+constexpr float kTrail = 8.0f;
+template <int DT> constexpr float kLift = DT == F16 ? 7.0f : 0.0f;
+
 // C += A B of 16 x 16 x 32: lane l holds A[l % 16][8 (l / 16) ..], B[..][l % 16]
 // of the same eight inner indices, C[4 (l / 16) ..][l % 16].
 template <int DT>

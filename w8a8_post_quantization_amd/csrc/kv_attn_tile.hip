@@ -316,11 +316,10 @@ __global__ __launch_bounds__(64 * NW, D == 64 ? 3 : D == 128 ? 2 : 1) void kv_ti
         for (int i = 1; i < 16; ++i) top = fmaxf(top, x[i]);
         return top * c;
     };
-    // The maximum that weights are taken against may trail the true one by 8
-    // (weights up to 256): rows are rescaled only where it is passed by more.
+    // Rows are rescaled only where the maximum trails by more than it may.
     const auto rescale = [&](float top) SQ_INLINE {
-        if (__any(top > m + 8.0f)) {
-            const float mn = fmaxf(m, fmaxf(top, __shfl_xor(top, 32, 64)));
+        if (__any(top > m + (kTrail + kLift<DT>))) {
+            const float mn = fmaxf(m, fmaxf(top, __shfl_xor(top, 32, 64)) - kLift<DT>);
             const float f = __builtin_amdgcn_exp2f(m - mn);
             m = mn;
             l *= f;
