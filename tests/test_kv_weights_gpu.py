@@ -59,3 +59,37 @@ def test_small_weights_add_up(fmt, dim, T, seqs, dt, nats, spread):
     got = attend(cache, q, dt, seqs, scale)
     err = np.abs(got - want)
     assert (err <= tol).all(), (err / tol).max()
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.0, 1e-42, -1e-42])
+@pytest.mark.parametrize("T", [1, 5, 70, 150])
+@pytest.mark.parametrize("fmt,dim", [("e2m1", 128), ("e4m3", 64), ("e2m1", 256)])
+def test_scales_of_zero_against_infinite_scores(fmt, dim, T, scale):
+    """A key of -2^17 is infinite in fp16.  Times a scale of 0 its score is NaN,
+    and so are the queries that see it, whichever kernel takes them; times the
+    least scales above and below 0 it is an infinity of its sign, whose weight
+    is 0 or, of +inf, NaN.  All others' scores are 0, or as good as."""
+    log(f"scale {scale} {fmt} {dim} {T}")
+    rng = np.random.default_rng(62)
+    n, at = 200, 190 - T // 2  # (about half of several queries see it)
+    q = to_dt(1.0 + rng.random((T, 2, dim)), "f16")
+    k, v = (rng.standard_normal((n, 2, dim)).astype(np.float32) for _ in range(2))
+    k[at, 0, :32] = 0.0
+    k[at, 0, 3] = -2.0 ** 17
+    cache = ref.Cache(rng, [n], 2, 16, dim, FMTS[fmt], k=[k], v=[v])
+    got = attend(cache, q, "f16", 1, scale)[0]
+    _, values = cache.read(0)
+    u = ref.HALF_STEP["f16"]
+    for i in range(T):
+        for h in range(2):
+            keys = np.arange(n - T + i + 1)
+            meets = h == 0 and at in keys
+            if meets and (scale <= 0):  # (-0.0 <= 0: 0 inf is NaN; a negative scale makes it +inf)
+                assert np.isnan(got[i, h]).all(), (i, h)
+                continue
+            if meets:
+                keys = keys[keys != at]
+            # equal weights, exact in the type: sums in fp32, the output rounded
+            want, a = values[keys, h].mean(axis=0), np.abs(values[keys, h]).mean(axis=0)
+            tol = (n + 64) * 2.0 ** -23 * a + u * np.abs(want) + 2.0 ** -25
+            assert (np.abs(got[i, h] - want) <= tol).all(), (i, h)

@@ -172,8 +172,12 @@ __global__ __launch_bounds__(64 * NW, D == 64 ? 3 : D == 128 ? 2 : 1) void kv_ti
     const int n_all = t_hi > t_lo ? (t_hi - t_base + KT - 1) / KT : 0;
     const int k0 = (int)((int64_t)n_all * split / splits), k1 = (int)((int64_t)n_all * (split + 1) / splits);
     const int n_tiles = k1 - k0;
-    // (a negative scale turns the queries; the maximum is taken before the scale)
-    const float c = fmaxf(fabsf(a.scale) * 1.44269504088896341f, 1e-37f);
+    // Scores are multiplied by c > 0 as their weights are formed (a negative scale
+    // turns the queries), behind hiding and maximum.  Of a scale of 0, where a
+    // hidden score of -inf would turn NaN, they are multiplied before, and c is 1.
+    const float to_log2 = fabsf(a.scale) * 1.44269504088896341f;
+    const bool early = to_log2 == 0.0f;
+    const float c = early ? 1.0f : to_log2;
     const int32_t *const table = tables + (int64_t)b * a.width;
     const int g_last = (t_hi - 1) >> 4;
 
@@ -301,8 +305,9 @@ __global__ __launch_bounds__(64 * NW, D == 64 ? 3 : D == 128 ? 2 : 1) void kv_ti
         for (int j = 0; j < JT; ++j) o[j] = mfma32<DT>(f[j], make_uint4(w.x, w.y, w.z, w.w), o[j]);
     };
     const auto hide = [&](f32x16 &x, int t) SQ_INLINE {
-        if (t < w_all_lo || t + 32 > w_all_hi) {
+        if (early || t < w_all_lo || t + 32 > w_all_hi) {
             asm volatile("");  // (a branch, not selects)
+            if (early) x *= to_log2;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 const int key = t + (i & 3) + 8 * (i >> 2) + 4 * hh;
