@@ -93,3 +93,41 @@ def test_scales_of_zero_against_infinite_scores(fmt, dim, T, scale):
             want, a = values[keys, h].mean(axis=0), np.abs(values[keys, h]).mean(axis=0)
             tol = (n + 64) * 2.0 ** -23 * a + u * np.abs(want) + 2.0 ** -25
             assert (np.abs(got[i, h] - want) <= tol).all(), (i, h)
+
+
+# a scale that is 1 as a power of two, once log2(e) is multiplied in fp32
+LN2 = float(np.float32(0.6931471824645996))
+
+
+@pytest.mark.parametrize("rise", [1, 2, 40, 128])
+@pytest.mark.parametrize("T,seqs,n", [(1, 300, 600), (5, 100, 600), (60, 1, 300), (150, 1, 400)])
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("fmt,dim", [("e4m3", 128), ("e4m3", 64), ("e4m3", 256)])
+def test_scores_a_step_of_fp32_apart(fmt, dim, dt, T, seqs, n, rise):
+    """Scores of 2^27 + 16 i (powers of two), i rising by 1 every `rise` keys:
+    neighbours in fp32, whose weights differ by 2^16.  Sums are exact."""
+    log(f"a step apart {fmt} {dim} {dt} {T} {seqs} {rise}")
+    assert np.float32(LN2) * np.float32(1.44269504088896341) == np.float32(1.0)
+    rng = np.random.default_rng(64)
+    q, k = np.zeros((T, 1, dim)), np.zeros((n, 1, dim), np.float32)
+    half = dim // 2
+    q[..., :half], k[..., :half] = 2.0 ** 11, 2.0 ** 16 / half  # 2^27
+    i = np.minimum(np.arange(n) // rise, 200)
+    # 16 i from two channels of a block of their own, by the fifteens and the rest
+    q[..., half], q[..., half + 1] = 16.0 * 15, 16.0
+    k[:, 0, half], k[:, 0, half + 1] = i // 15, i % 15
+    q = to_dt(q, dt)
+    v = rng.standard_normal((n, 1, dim)).astype(np.float32)
+    cache = ref.Cache(rng, [n], 1, 16, dim, FMTS[fmt], k=[k], v=[v])
+    keys, values = cache.read(0)
+    assert np.array_equal(keys, k)  # (the format holds them)
+    got, u, least = attend(cache, q, dt, seqs, LN2), ref.HALF_STEP[dt], 2.0 ** -25 if dt == "f16" else 0.0
+    for t in range(T):
+        m = n - T + t + 1
+        w = np.exp2(16.0 * (i[:m] - i[:m].max()))
+        w /= w.sum()
+        want, a = w @ values[:m, 0], w @ np.abs(values[:m, 0])
+        tol = (u + (n + 64) * 2.0 ** -23) * a * (1 + u) + u * np.abs(want) + least
+        tol = tol + least * np.abs(values[:m, 0]).sum(axis=0)
+        err = np.abs(got[:, t, 0] - want)
+        assert (err <= tol).all(), (t, (err / tol).max())

@@ -327,7 +327,7 @@ __global__ __launch_bounds__(256, (blocks_per_cu(D, FMT, NT))) void kv_attn_kern
 #pragma unroll
                 for (int i = 0; i < 8; ++i) top = fmaxf(top, x[nt][i]);
                 // Rows are rescaled only where the maximum trails by more than it may.
-                if (__any(top > m[nt] + (kTrail + kLift<DT>))) {
+                if (__any(top - m[nt] > kTrail + kLift<DT>)) {
                     top = fmaxf(top, __shfl_xor(top, 16, 64));
                     top = fmaxf(top, __shfl_xor(top, 32, 64));
                     const float mn = fmaxf(m[nt], top - kLift<DT>);

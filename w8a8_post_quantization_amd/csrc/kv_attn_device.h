@@ -23,7 +23,9 @@ constexpr float kNoMax = -3.402823466e38f;
 // are lifted to the upper end, 2^(kTrail + kLift) = 2^15 at the most: those of
 // 2^-21 of the largest have all their bits, those of 2^-32 are lost (unlifted,
 // 3500 keys of 2^-26 each, 18 nats below the first, came out up to 10 bounds
-// off).  bf16 has fp32's range.
+// off).  bf16 has fp32's range.  (The difference of score and m is compared, not m
+// plus the slack: where fp32's step is 16 that sum is rounded to the next score,
+// whose weight would be 2^16.)
 constexpr float kTrail = 8.0f;
 template <int DT> constexpr float kLift = DT == F16 ? 7.0f : 0.0f;
 

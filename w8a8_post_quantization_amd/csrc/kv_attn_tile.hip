@@ -323,7 +323,7 @@ __global__ __launch_bounds__(64 * NW, D == 64 ? 3 : D == 128 ? 2 : 1) void kv_ti
     };
     // Rows are rescaled only where the maximum trails by more than it may.
     const auto rescale = [&](float top) SQ_INLINE {
-        if (__any(top > m + (kTrail + kLift<DT>))) {
+        if (__any(top - m > kTrail + kLift<DT>)) {
             const float mn = fmaxf(m, fmaxf(top, __shfl_xor(top, 32, 64)) - kLift<DT>);
             const float f = __builtin_amdgcn_exp2f(m - mn);
             m = mn;
