@@ -131,3 +131,48 @@ def test_scores_a_step_of_fp32_apart(fmt, dim, dt, T, seqs, n, rise):
         tol = tol + least * np.abs(values[:m, 0]).sum(axis=0)
         err = np.abs(got[:, t, 0] - want)
         assert (err <= tol).all(), (t, (err / tol).max())
+
+
+@pytest.mark.parametrize("order", ["random", "rising", "falling"])
+@pytest.mark.parametrize("exponent", [20, 24, 27, 28, 31, 40, 90])
+@pytest.mark.parametrize("T,seqs,n", [(1, 300, 600), (5, 100, 600), (60, 1, 300), (150, 1, 400), (60, 1, 3000)])
+@pytest.mark.parametrize("fmt,dim,dt", [("e4m3", 128, "f16"), ("e4m3", 64, "bf16"), ("e4m3", 256, "f16"),
+                                        ("e4m3", 128, "bf16")])
+def test_scores_of_any_size(fmt, dim, dt, T, seqs, n, exponent, order):
+    """Keys of 8/8 .. 14/8 along one direction, scores of up to 14/8 2^exponent
+    of either sign; every third query is 2^-18 of the others, its scores
+    moderate where theirs are largest.
+
+    All products and sums are exact in fp32.  Scores past 2^12 are equal or a
+    fourteenth apart, where the lesser's weight is 0 in fp32: such rows are means of
+    the keys with the largest, off by the roundings of equal weights.  Others'
+    scores are off by three roundings, 2^-21.  The bound's other terms are those of
+    ref.attention."""
+    log(f"large scores {fmt} {dim} {dt} {T} {seqs} {exponent} {order} {n}")
+    rng = np.random.default_rng(63)
+    step = rng.integers(8, 15, n)
+    step = {"random": step, "rising": np.sort(step), "falling": np.sort(step)[::-1]}[order]
+    d = np.sign(rng.standard_normal(dim)).astype(np.float32)
+    k = (step[:, None, None] / 8.0 * d).astype(np.float32)
+    v = rng.standard_normal((n, 1, dim)).astype(np.float32)
+    size = np.where(np.arange(T) % 3 == 1, 2.0 ** -14, 16.0)[:, None, None] * np.array([1.0, -1.0])[None, :, None]
+    q = to_dt(size * d, dt)
+    cache = ref.Cache(rng, [n], 1, 16, dim, FMTS[fmt], k=[k], v=[v])
+    keys, values = cache.read(0)
+    assert np.array_equal(keys, k)  # (the format holds them)
+    scale = 2.0 ** exponent / (16.0 * dim)
+    got, want, tol = attend(cache, q, dt, seqs, scale), np.zeros((T, 2, dim)), np.zeros((T, 2, dim))
+    u, least = ref.HALF_STEP[dt], 2.0 ** -25 if dt == "f16" else 0.0
+    for i in range(T):
+        see = slice(0, n - T + i + 1)
+        for h in range(2):
+            s = (keys[see, 0] @ mx.to_f32(q[i, h]).astype(np.float64)) * scale
+            w = np.exp(s - s.max())
+            w /= w.sum()
+            a, top = w @ np.abs(values[see, 0]), np.abs(s).max()
+            off = 0.0 if top > 4096 else np.expm1(2 * 3 * 2.0 ** -23 * top)
+            want[i, h] = w @ values[see, 0]
+            tol[i, h] = (u + off + (n + 64) * 2.0 ** -23) * a * (1 + u) + u * np.abs(want[i, h])
+            tol[i, h] += least + least * np.abs(values[see, 0]).sum(axis=0)
+    err = np.abs(got - want)
+    assert (err <= tol).all(), (err / tol).max()

@@ -172,12 +172,16 @@ __global__ __launch_bounds__(64 * NW, D == 64 ? 3 : D == 128 ? 2 : 1) void kv_ti
     const int n_all = t_hi > t_lo ? (t_hi - t_base + KT - 1) / KT : 0;
     const int k0 = (int)((int64_t)n_all * split / splits), k1 = (int)((int64_t)n_all * (split + 1) / splits);
     const int n_tiles = k1 - k0;
-    // Scores are multiplied by c > 0 as their weights are formed (a negative scale
-    // turns the queries), behind hiding and maximum.  Of a scale of 0, where a
-    // hidden score of -inf would turn NaN, they are multiplied before, and c is 1.
+    // Scores are multiplied by c > 0 as their weights are formed, in one operation
+    // with the maximum's subtraction (a negative scale turns the queries), behind
+    // hiding and maximum.  Where that does not serve they are multiplied earlier,
+    // and c is 1: with a scale of 0, as a hidden score of -inf would turn NaN; and
+    // once a row's maximum passes 2^20, since it is rounded and the product is not,
+    // so that a weight is 2^(half fp32's step there) off.
     const float to_log2 = fabsf(a.scale) * 1.44269504088896341f;
-    const bool early = to_log2 == 0.0f;
-    const float c = early ? 1.0f : to_log2;
+    constexpr float kEarly = 1048576.0f;
+    bool early = to_log2 == 0.0f;
+    const auto factor = [&]() SQ_INLINE { return early ? 1.0f : to_log2; };  // c
     const int32_t *const table = tables + (int64_t)b * a.width;
     const int g_last = (t_hi - 1) >> 4;
 
@@ -319,10 +323,10 @@ __global__ __launch_bounds__(64 * NW, D == 64 ? 3 : D == 128 ? 2 : 1) void kv_ti
         float top = x[0];
 #pragma unroll
         for (int i = 1; i < 16; ++i) top = fmaxf(top, x[i]);
-        return top * c;
+        return top * factor();
     };
     // Rows are rescaled only where the maximum trails by more than it may.
-    const auto rescale = [&](float top) SQ_INLINE {
+    const auto rescale = [&](f32x16 &x, float top) SQ_INLINE {
         if (__any(top - m > kTrail + kLift<DT>)) {
             const float mn = fmaxf(m, fmaxf(top, __shfl_xor(top, 32, 64)) - kLift<DT>);
             const float f = __builtin_amdgcn_exp2f(m - mn);
@@ -330,12 +334,16 @@ __global__ __launch_bounds__(64 * NW, D == 64 ? 3 : D == 128 ? 2 : 1) void kv_ti
             l *= f;
 #pragma unroll
             for (int j = 0; j < JT; ++j) o[j] *= f;
+            if (!early && __any(fabsf(mn) > kEarly && mn != kNoMax)) {
+                early = true;
+                x *= to_log2;
+            }
         }
     };
     const auto form_weights = [&](f32x16 &x, Weights &w) SQ_INLINE {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], c, -m));
+            x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], factor(), -m));
             l += x[i];
         }
 #pragma unroll
@@ -395,7 +403,7 @@ __global__ __launch_bounds__(64 * NW, D == 64 ? 3 : D == 128 ? 2 : 1) void kv_ti
         multiply_keys(x[0], kf);
         read_keys(kf, 0, 1, 0, S / 2);
         hide(x[0], tile_at(0));
-        rescale(largest(x[0]));
+        rescale(x[0], largest(x[0]));
         wait_vmcnt<0>();  // (else the queries' loads count as pending in the loop)
         for (int i = 0; i < n_tiles; ++i) {
             const int t = tile_at(i), slot = i & 1;
@@ -445,7 +453,7 @@ __global__ __launch_bounds__(64 * NW, D == 64 ? 3 : D == 128 ? 2 : 1) void kv_ti
                     // whether it ran or not)
                     wait_vmcnt<0>();
                 }
-                rescale(top);
+                rescale(x[~u & 1], top);
             };
             unit(std::integral_constant<int, 0>{});
             unit(std::integral_constant<int, 1>{});
