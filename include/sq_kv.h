@@ -21,8 +21,9 @@
  *
  * Alignment: all of q, k, v, y, kq, vq, their rows' strides in bytes, the
  * multipliers and the workspace 16 bytes; ks, vs 4 bytes; other arrays their
- * element size.  Inputs and outputs do not overlap,
- * nor do outputs (the cache's keys and values, a call's k and v) one another.
+ * element size.  What a call writes (the workspace and, in a write, the cache's
+ * four arrays among it) shares no byte with what it reads or with one another:
+ * SQ_ERR_ARG.
  */
 #ifndef SQ_KV_H
 #define SQ_KV_H

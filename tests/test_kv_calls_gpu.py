@@ -572,3 +572,46 @@ def test_the_binding_refuses_outputs_that_are_one():
     with pytest.raises(sq.SQError):
         sq.dequantize_kv_mx(c, torch.zeros(1, 1, dtype=torch.int32, device="cuda"),
                             torch.tensor([0, 3], dtype=torch.int32, device="cuda"), 3, out=(k, k))
+
+
+def test_outputs_inside_inputs_refuse_and_neighbours_do_not():
+    """Outputs that begin inside the queries, or lie in part over one another,
+    are refused; ones that end where an input begins, or lie in the gap between
+    two heads' queries, are not."""
+    import torch
+
+    log("outputs beside and inside inputs")
+    T, heads, dim, n = 6, 2, 64, 6 * 2 * 64
+    c = sq.new_kv_cache_mx(4, heads, 16, dim)
+    table = torch.arange(4, dtype=torch.int32, device="cuda").view(1, 4)
+    lens, cu = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([20], [0, T]))
+    k = torch.randn(20, heads, dim, device="cuda", dtype=torch.float16)
+    sq.rope_quantize_kv_mx(None, k, k, torch.arange(20, device="cuda"), c)
+    buf = torch.randn(4 * n, device="cuda", dtype=torch.float16)
+    rows = lambda at: buf[at:at + n].view(T, heads, dim)  # noqa: E731
+    att = lambda q, **kw: sq.attention_kv_mx(q, c, table, lens, cu, max_q=T, **kw)  # noqa: E731
+    write = lambda q, **kw: sq.rope_quantize_kv_mx(q, k[:T], k[:T], torch.full((T,), -1, device="cuda"), c, **kw)  # noqa: E731
+    q = rows(n)
+    want, turned = att(q.clone()), write(q.clone())
+    for at in (n - 8, n + 8, 2 * n - 8, 8):
+        for call in (att, write):
+            with pytest.raises(sq.SQError):
+                call(q, out=rows(at))
+        with pytest.raises(sq.SQError):
+            sq.dequantize_kv_mx(c, table, cu, T, out=(rows(n), rows(at)))
+    saved = q.clone()
+    for at in (0, 2 * n):
+        for call, w in ((att, want), (write, turned)):
+            y = call(q, out=rows(at))
+            torch.cuda.synchronize()
+            assert torch.equal(y, w) and torch.equal(q, saved)
+    # head 0's queries, room for an output, head 1's
+    far = torch.as_strided(buf, (T, heads, dim), (dim, T * dim + n, 1), 0)
+    far.copy_(saved)
+    for call, w in ((att, want), (write, turned)):
+        y = call(far, out=rows(T * dim))
+        torch.cuda.synchronize()
+        assert torch.equal(y, w) and torch.equal(far, saved)
+        for at in (T * dim - 8, T * dim + 8):
+            with pytest.raises(sq.SQError):
+                call(far, out=rows(at))

@@ -137,6 +137,93 @@ def test_outputs_that_are_one_refuse():
     assert L.sq_dequantize_kv_mx(cache(), FAKE, 2, 3, FAKE, 9, FAKE, FAKE, sq.SQ_BF16, None) == ARG
 
 
+# Operands at addresses of their own, never read: (name, address, bytes).
+def _apart(sizes):
+    at, out = 1 << 32, {}
+    for name, n in sizes.items():
+        out[name] = (at, n)
+        at += (n + 4095) // 4096 * 4096 + 4096
+    return out
+
+
+def _meeting(places, first, second):
+    """Addresses of `second` that share some bytes with `first`: its last bytes
+    on the first's first, its first on the first's last, and inside."""
+    at, n = places[first]
+    m = places[second][1]
+    return [at - (m - 16) // 16 * 16, at + (n - 16) // 16 * 16, at]
+
+
+def _assert_pairs_refuse(call, places, outputs):
+    pairs = 0
+    for out in outputs:
+        for name in places:
+            if name == out:
+                continue
+            for at in _meeting(places, out, name):
+                moved = {k: p for k, (p, _) in places.items()}
+                moved[name] = at
+                assert call(moved) == ARG, (out, name, at - places[out][0])
+                pairs += 1
+    return pairs
+
+
+CACHE_BYTES = dict(kq=4 * 2 * 16 * 64, ks=4 * 2 * 16 * 4, vq=4 * 2 * 16 * 64, vs=4 * 2 * 16 * 4)
+
+
+def _cache_at(p):
+    return cache(kq=p["kq"], ks=p["ks"], vq=p["vq"], vs=p["vs"])
+
+
+@built
+def test_outputs_of_a_write_that_meet_refuse():
+    """The rotated queries and the four arrays of the cache, in part over one
+    another or over what a write reads."""
+    L = sq.lib()
+    T = 40  # (queries, keys and values as thirds of rows of 12 heads of 128, 2 bytes each)
+    rows = (T - 1) * 12 * 128 * 2
+    places = _apart(dict(q=rows + 8 * 256, k=rows + 2 * 256, v=rows + 2 * 256, pos=8 * T, freq=8 * 32, qm=4 * 8 * 128,
+                         km=4 * 2 * 128, slots=8 * T, out=T * 8 * 256, **CACHE_BYTES))
+    s = strides(12 * 128, 128)
+
+    def call(p):
+        return L.sq_rope_quantize_kv_mx(p["q"], s, p["k"], s, p["v"], s, sq.SQ_F16, T, 8, p["pos"], p["freq"], 64, 1.0,
+                                        0, p["qm"], p["km"], p["slots"], _cache_at(p), p["out"], None)
+
+    assert _assert_pairs_refuse(call, places, ["out", "kq", "ks", "vq", "vs"]) == 5 * 12 * 3
+
+
+@built
+def test_outputs_of_a_read_that_meet_refuse():
+    L = sq.lib()
+    places = _apart(dict(table=4 * 6, cu=4 * 3, k=9 * 2 * 256, v=9 * 2 * 256, **CACHE_BYTES))
+
+    def call(p):
+        return L.sq_dequantize_kv_mx(_cache_at(p), p["table"], 2, 3, p["cu"], 9, p["k"], p["v"], sq.SQ_BF16, None)
+
+    assert _assert_pairs_refuse(call, places, ["k", "v"]) == 2 * 7 * 3
+
+
+@built
+def test_outputs_of_an_attention_that_meet_refuse():
+    """Its output and workspace; queries as rows of a wider product, and as
+    heads far apart."""
+    L = sq.lib()
+    T, B, width = 40, 2, 3
+    need = L.sq_attention_kv_mx_workspace(T, 8, cache(), B, width, 9)
+    assert need > 0
+    for token, head in ((12 * 128, 128), (128, 64 * 128)):
+        q = (T - 1) * token * 2 + 7 * head * 2 + 256
+        places = _apart(dict(q=q, table=4 * B * width, lens=4 * B, cu=4 * (B + 1), y=T * 8 * 256, ws=need,
+                             **CACHE_BYTES))
+
+        def call(p):
+            return L.sq_attention_kv_mx(p["q"], strides(token, head), sq.SQ_BF16, T, 8, _cache_at(p), p["table"], B,
+                                        width, p["lens"], p["cu"], 9, 0.1, 1, 0, p["y"], p["ws"], need, None)
+
+        assert _assert_pairs_refuse(call, places, ["y", "ws"]) == 2 * 9 * 3
+
+
 @built
 def test_workspace_sizes():
     """Enough for the parts of the blocks, whatever the lengths: it depends on

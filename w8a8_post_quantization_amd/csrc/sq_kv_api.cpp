@@ -72,6 +72,45 @@ int check_attention(int64_t T, int64_t q_heads, const sq::KvCache &c, int64_t B,
     return SQ_OK;
 }
 
+// The bytes of a dense operand.
+struct Span {
+    int64_t at, n;
+};
+inline Span span(const void *p, int64_t n) { return {(int64_t)(uintptr_t)p, p ? n : 0}; }
+inline bool meet(const Span &a, const Span &b) { return a.n && b.n && a.at < b.at + b.n && b.at < a.at + a.n; }
+
+// Whether an output meets any of these, or one of [T, heads] strided rows of n
+// bytes.  Rows are looked at a head at a time where the output lies between the
+// first's beginning and the last's end: it may lie between rows.
+template <int N>
+bool meet_any(const Span &out, const Span (&in)[N]) {
+    for (const Span &s : in)
+        if (meet(out, s)) return true;
+    return false;
+}
+bool meet_rows(const Span &out, const void *x, const int64_t stride[2], int dt, int64_t T, int64_t heads, int64_t n) {
+    const int64_t at = (int64_t)(uintptr_t)x, token = stride[0] * (int64_t)esize(dt), head = stride[1] * (int64_t)esize(dt);
+    if (!meet(out, {at, (T - 1) * token + (heads - 1) * head + n})) return false;
+    for (int64_t h = 0; h < heads; ++h) {
+        const int64_t first = at + h * head;
+        // the first token whose row ends behind the output's beginning
+        const int64_t short_of = out.at - n - first;
+        const int64_t t = short_of < 0 ? 0 : token ? short_of / token + 1 : T;
+        if (t < T && first + t * token < out.at + out.n) return true;
+    }
+    return false;
+}
+
+// The bytes of the cache's arrays, keys first.
+struct CacheSpans {
+    Span kq, ks, vq, vs;
+};
+CacheSpans cache_spans(const sq_kv_cache *c) {
+    const int64_t rows = c->pages * c->page * c->heads, codes = c->fmt == SQ_MX_E2M1 ? c->dim / 2 : c->dim;
+    return {span(c->kq, rows * codes), span(c->ks, rows * (c->dim / 32)), span(c->vq, rows * codes),
+            span(c->vs, rows * (c->dim / 32))};
+}
+
 // No sequence has more queries than there are.
 int64_t most_queries(int64_t max_q, int64_t T) { return max_q < T ? max_q : T; }
 
@@ -105,8 +144,24 @@ int sq_rope_quantize_kv_mx(const void *q, const int64_t q_stride[2], const void 
     if (!slots || (rotary && (!positions || !inv_freq))) return SQ_ERR_NULL;
     if (!aligned(slots, 8) || !aligned(k_mul, 16) || !aligned(positions, 8) || !aligned(inv_freq, 8))
         return SQ_ERR_ALIGN;
-    // (keys and values would be written over one another)
-    if (cache->kq == cache->vq || cache->ks == cache->vs) return SQ_ERR_ARG;
+    // Nothing that the call writes lies over what it reads or over one another.
+    const CacheSpans c = cache_spans(cache);
+    const int64_t row = cache->dim * (int64_t)esize(dt);
+    const Span out = span(q ? q_out : nullptr, T * q_heads * row);
+    const Span written[5] = {c.kq, c.ks, c.vq, c.vs, out};
+    const Span read[5] = {span(slots, T * 8), span(rotary ? positions : nullptr, T * 8),
+                          span(rotary ? inv_freq : nullptr, rotary / 2 * 8),
+                          span(q ? q_mul : nullptr, q_heads * cache->dim * 4),
+                          span(k_mul, cache->heads * cache->dim * 4)};
+    for (int i = 0; i < 5; ++i) {
+        if (!written[i].n) continue;
+        for (int j = 0; j < i; ++j)
+            if (meet(written[i], written[j])) return SQ_ERR_ARG;
+        if (meet_any(written[i], read) || meet_rows(written[i], k, k_stride, dt, T, cache->heads, row) ||
+            meet_rows(written[i], v, v_stride, dt, T, cache->heads, row) ||
+            (q && meet_rows(written[i], q, q_stride, dt, T, q_heads, row)))
+            return SQ_ERR_ARG;
+    }
     a.q = q;
     a.k = k;
     a.v = v;
@@ -144,7 +199,11 @@ int sq_dequantize_kv_mx(const sq_kv_cache *cache, const int32_t *table, int64_t 
     if (const int e = check_arrays(cache)) return e;
     if (!cu || !k || !v || (width && !table)) return SQ_ERR_NULL;
     if (!aligned(k, 16) || !aligned(v, 16) || !aligned(table, 4) || !aligned(cu, 4)) return SQ_ERR_ALIGN;
-    if (k == v) return SQ_ERR_ARG;  // (written over one another)
+    const CacheSpans c = cache_spans(cache);
+    const int64_t dense = total * cache->heads * cache->dim * (int64_t)esize(dt);
+    const Span out_k = span(k, dense), out_v = span(v, dense);
+    const Span read[6] = {c.kq, c.ks, c.vq, c.vs, span(table, B * width * 4), span(cu, (B + 1) * 4)};
+    if (meet(out_k, out_v) || meet_any(out_k, read) || meet_any(out_v, read)) return SQ_ERR_ARG;
     a.table = table;
     a.width = width;
     a.cu = cu;
@@ -188,6 +247,14 @@ int sq_attention_kv_mx(const void *q, const int64_t q_stride[2], int dt, int64_t
                                                    width << a.cache.page_log, most);
     if (need && (!workspace || workspace_bytes < need)) return SQ_ERR_WORKSPACE;
     if (!aligned(workspace, 16)) return SQ_ERR_ALIGN;
+    const CacheSpans c = cache_spans(cache);
+    const int64_t row = cache->dim * (int64_t)esize(dt);
+    const Span out = span(y, T * q_heads * row), work = span(workspace, (int64_t)need);
+    const Span read[7] = {c.kq, c.ks, c.vq, c.vs, span(table, B * width * 4), span(seq_lens, B * 4),
+                          span(cu_q, (B + 1) * 4)};
+    if (meet(out, work) || meet_any(out, read) || meet_any(work, read) ||
+        meet_rows(out, q, q_stride, dt, T, q_heads, row) || (need && meet_rows(work, q, q_stride, dt, T, q_heads, row)))
+        return SQ_ERR_ARG;
     a.q = q;
     a.q_st = q_stride[0];
     a.q_sh = q_stride[1];
