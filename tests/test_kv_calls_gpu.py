@@ -615,3 +615,31 @@ def test_outputs_inside_inputs_refuse_and_neighbours_do_not():
         for at in (T * dim - 8, T * dim + 8):
             with pytest.raises(sq.SQError):
                 call(far, out=rows(at))
+
+
+def test_whole_numbers_past_64_bits():
+    """A window or a number of queries past 64 bits is as good as none, a
+    rotary layout of that kind is no layout."""
+    import torch
+
+    log("numbers past 64 bits")
+    rng = np.random.default_rng(71)
+    cache = ref.Cache(rng, [90, 70], 2, 16, 64, mx.E2M1)
+    held, table = on_gpu(torch, cache.arrays()), dev(cache.table, torch)
+    q = torch.randn(45, 4, 64, device="cuda", dtype=torch.bfloat16)
+    n, cu = dev(np.array([90, 70], np.int32), torch), dev(np.array([0, 40, 45], np.int32), torch)
+    call = lambda **kw: sq.attention_kv_mx(q, held, table, n, cu, out=torch.full_like(q, 3.0), **kw)  # noqa: E731
+    want, most, need = call(max_q=40), call(), sq.attention_kv_mx_workspace(45, 4, held, 2, table.shape[1], 45)
+    for big in ((1 << 64) + 1, 1 << 64, (1 << 63) + 1, 1 << 80):
+        y, z = call(max_q=40, window=big), call(max_q=big)
+        torch.cuda.synchronize()
+        assert torch.equal(y.view(torch.int16), want.view(torch.int16)), big
+        assert torch.equal(z.view(torch.int16), most.view(torch.int16)), big
+        assert sq.attention_kv_mx_workspace(45, 4, held, 2, table.shape[1], big) == need
+        with pytest.raises(sq.SQError):
+            sq.rope_quantize_kv_mx(q, q[:, :2], q[:, 2:], torch.full((45,), -1, device="cuda"), held, layout=big)
+    for small in (-1, -(1 << 64) + 1, -(1 << 80)):
+        for kw in (dict(window=small), dict(max_q=small)):
+            with pytest.raises(ValueError):
+                call(**kw)
+        assert sq.attention_kv_mx_workspace(45, 4, held, 2, table.shape[1], small) == 0

@@ -60,6 +60,7 @@ class _KvCache(ctypes.Structure):
 
 _CACHE_P = ctypes.POINTER(_KvCache)
 _Strides2, _Strides6 = _I64 * 2, _I64 * 6
+_MOST = (1 << 63) - 1
 
 SIGNATURES = {
     "sq_status_str": (ctypes.c_char_p, [_I]),
@@ -854,7 +855,7 @@ def rope_quantize_kv_mx(q, k, v, slots, cache, fmt=SQ_MX_E2M1, positions=None, i
     _mx_call("sq_rope_quantize_kv_mx",
              (k, v, q, slots, positions if rotary else None, inv_freq, q_mul, k_mul, y, *cache),
              (qp, at, k.data_ptr(), at + 16, v.data_ptr(), at + 32, _dt_codes[dt], T, q_heads, pp, fp,
-              rotary, amplitude, layout, qm, km, sp, c, yp), stream)
+              rotary, amplitude, layout if 0 <= layout <= 1 else -1, qm, km, sp, c, yp), stream)
     return y
 
 
@@ -890,6 +891,7 @@ def dequantize_kv_mx(cache, table, cu, total, fmt=SQ_MX_E2M1, out_dtype=None, ou
 
 def attention_kv_mx_workspace(T, q_heads, cache, B, width, max_q, fmt=SQ_MX_E2M1) -> int:
     """Bytes of workspace of such an attention_kv_mx call."""
+    max_q = max(-1, min(max_q, T))  # (the C call's numbers have 64 bits)
     return int(lib().sq_attention_kv_mx_workspace(T, q_heads, _kv_cache(cache, fmt), B, width, max_q))
 
 
@@ -925,10 +927,13 @@ def attention_kv_mx(q, cache, table, seq_lens, cu_q=None, fmt=SQ_MX_E2M1, max_q=
         max_q = T
     elif max_q < 1:
         raise ValueError(f"max_q {max_q}")
+    else:
+        max_q = min(max_q, max(T, 1))  # (the C call's numbers have 64 bits)
     if scale is None:
         scale = dim ** -0.5
     if window < 0:
         raise ValueError(f"window {window}")
+    window = min(window, _MOST)
     y = _kv_result(out, "out", (T, q_heads, dim), q.dtype, q.device, stream)
     if y.data_ptr() == q.data_ptr() and T:
         raise ValueError("out is q")
