@@ -101,7 +101,9 @@ int sq_dequantize_kv_mx(const sq_kv_cache *cache, const int32_t *table, int64_t 
  * magnitudes from 65520 on become infinite).  Products are summed in fp32, the softmax's
  * maximum and sum are fp32; its weights are rounded to dt for the product with
  * the values (in fp16 those below 2^-21 of a row's largest by up to 2^-32 of
- * it).
+ * it).  They are at most 2^15 in fp16 and 2^8 in bf16 before they are divided by
+ * their sum, so that bf16 values of 2^120 over their number and more may give
+ * an infinity for a finite mean.
  *   q        [T, q_heads, dim] of dt (SQ_F16 or SQ_BF16), strides as above
  *   table    int32 [B, width], seq_lens int32 [B]
  *   cu_q     int32 [B + 1], not descending from 0, cu_q[B] <= T; or NULL: T ==

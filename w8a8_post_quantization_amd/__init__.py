@@ -711,7 +711,10 @@ def rope_frequencies(rotary, base=10000.0, scaling=None, factor=1.0, original=No
       "ntk"     the base raised so that the slowest frequency is divided by it
       "yarn"    frequencies that turn fewer than `slow` times in the original
                 length divided by the factor, those that turn more than `fast`
-                times kept, a ramp between; amplitude 0.1 ln(factor) + 1"""
+                times kept, a ramp between that is linear in the number of
+                turns; amplitude 0.1 ln(factor) + 1
+    A model that was tuned with others (a ramp over i between the channels of
+    `slow` and `fast` turns, say) passes its own: any fp64 tensor serves."""
     if rotary < 2 or rotary % 2:
         raise ValueError(f"{rotary} rotated channels: an even number is needed")
     if scaling not in (None, "linear", "ntk", "yarn"):
@@ -812,9 +815,10 @@ def rope_quantize_kv_mx(q, k, v, slots, cache, fmt=SQ_MX_E2M1, positions=None, i
     """Rotary positions, and keys and values quantized into the cache: rows of
     k and v [T, heads, dim] go to slots [T] int64 (page * page size + place;
     others, as -1, are not written), the rotated q [T, q_heads, dim] (None: keys
-    and values alone) is returned.  positions [T] int64 and inv_freq fp64
-    [rotary/2] (rope_frequencies; None: nothing is rotated), the first `rotary`
-    channels; q_mul, k_mul fp32 [heads, dim]: smoothing, after the rotation."""
+    and values alone) is returned, in `out` if given (which shares no memory with
+    an input).  positions [T] int64 and inv_freq fp64 [rotary/2]
+    (rope_frequencies; None: nothing is rotated), the first `rotary` channels;
+    q_mul, k_mul fp32 [heads, dim]: smoothing, after the rotation."""
     c = _kv_cache(cache, fmt)
     heads, dim = c.heads, c.dim
     dt = k.dtype

@@ -22,10 +22,10 @@
 //
 // 64 tokens over 130 .. 32768 keys, 64 / 8 heads of 128, e2m1: 86 us, 425 MB at
 // 4.9 TB/s (without the arithmetic, in a copy for timing, 74); with codes loaded
-// to registers it was 147.  A wave issues 252 vector, 107 scalar and 23 LDS
-// instructions for 32 keys, which fill 58 % of the vector units' cycles.  16
-// tokens over 900 .. 2300 keys, 56 heads of 128, e4m3: 63 us, 5.7 TB/s.  One
-// token over 2049 keys, 64 / 8 heads: 7.7 us and 4.1 of the joining kernel.
+// to registers it was 147.  A wave issues 253 vector, 108 scalar and 23 LDS
+// instructions for 32 keys, which fill 59 % of the vector units' cycles.  16
+// tokens over 900 .. 2300 keys, 56 heads of 128, e4m3: 64 us, 5.6 TB/s.  One
+// token over 2049 keys, 64 / 8 heads: 7.7 us and 3.9 of the joining kernel.
 #include "kv_attn_device.h"
 
 namespace sq {
@@ -616,6 +616,11 @@ static Plan plan_attention(int64_t T, int q_heads, int heads, int dim, int fmt, 
         // waves a SIMD, three of 64 channels, one of 256).  Where there are less
         // than half of them, the keys of each tile are split over blocks (64 tokens
         // over 32768 keys, 64 / 8 heads: 85 us and 12 of the join, unsplit 882).
+        // Keys are the table's, the lengths being on the GPU: with one 131072 wide
+        // 5 x 64 tokens over 300 .. 600 keys take 25 and 9 us, with one as wide as
+        // the longest 27 and 7.  16 splits at the most leave CUs idle where a long
+        // context has few tiles of rows (48 heads on one key head, one token over
+        // 131072 keys: 16 blocks, 254 and 10 us).
         const int64_t slots = kCus * (dim == 64 ? 3 : dim == 128 && p.waves == 4 ? 2 : 1);
         const int64_t tiles = (T * group + 32 * p.waves - 1) / (32 * p.waves) * heads;
         int64_t splits = slots / tiles;

@@ -18,11 +18,13 @@
 // scores' maximum is taken.  Operands are read from LDS half a unit ahead.  Keys
 // and values have two slots in LDS each, with two barriers a tile.
 //
-// A prompt of 8192, 64 / 8 heads of 128, e2m1, 1.1 TFLOP: 1251 .. 1327 us over
-// runs, 0.83 .. 0.88 PFLOP/s (a library product of 8192^3 in bf16 1.21), the
-// matrix cores busy 46 % of the cycles, the vector units 52 %, LDS 36 %.  Four
-// waves of 64 rows, which read LDS half as often, took 2222.  8192 tokens of
-// 32 / 4 heads of 64: 458 us, of 16 / 4 heads of 256: 893.
+// A prompt of 8192, 64 / 8 heads of 128, e2m1, 1.1 TFLOP: 2.4 million cycles,
+// which are 1207 .. 1313 us under the profiler (2.01 .. 1.86 GHz) and 1075 ..
+// 1095 without, 0.84 .. 1.02 PFLOP/s (a library product of 8192^3 in bf16 1.21);
+// e4m3 1285 and fp16 1283 where it took 1250.  The matrix cores are busy 46 % of
+// the cycles, the vector units 53 %, LDS 36 %.  Four waves of 64 rows, which read
+// LDS half as often, took 2222.  8192 tokens of 32 / 4 heads of 64: 403 .. 469
+// us, of 16 / 4 heads of 256: 824 .. 921.
 #include <type_traits>
 
 #include "kv_attn_device.h"
